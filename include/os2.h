@@ -384,6 +384,109 @@ os2_status os2_peak_probe(int kind, int iters, int check, int32_t *result, doubl
 os2_status os2_gemm_noalloc(int m, int n, int k, const double *A, int lda, const double *B,
                             int ldb, double *C, int ldc, int num_moduli, int mode, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of a language model's vocabulary head, beside the method (the
+ * pages have no counterpart): the 8-bit integer product with scales that such
+ * a head is served with, the softmax cross entropy it is trained with and the
+ * AdamW step that trains it.  Conventions as above: device pointers owned by
+ * the caller, argument errors returned before anything is enqueued, everything
+ * enqueued on `stream`, errors found on the device in the status word.
+ * Leading dimensions count entries. */
+typedef enum {
+  OS2_F32 = 0,
+  OS2_F16 = 1,
+  OS2_BF16 = 2
+} os2_dtype;
+
+/* 8-bit integers of a matrix, one scale a row (a token's, an output channel's):
+ *   scale[i] = max_h |X_ih| / 127,   q_ih = rint(X_ih / scale[i]) in [-127, 127],
+ * each operation correctly rounded in FP32.  X is m x k row-major of `dtype`
+ * (os2_dtype), q m x k int8 with ldq >= k.  A row of zeros has scale 0 and
+ * integers 0; a row that holds Inf or NaN has scale NaN and integers 0, so what
+ * is computed from it is NaN.  (A row's largest magnitude below 127 2^-149 has
+ * scale 0 too.) */
+os2_status os2_quantize_rows(int m, int k, int dtype, const void *X, int ldx, int8_t *q, int ldq,
+                             float *scale, void *stream);
+
+/* Device workspace of os2_i8gemm and os2_i8linear (0 on bad args); B and ldb as
+ * in the call (their alignment decides; B is not read).  256-byte aligned. */
+size_t os2_i8gemm_workspace_size(int m, int n, int k, const void *B, int ldb);
+
+/* C_ij = (sum_h A_ih B_jh) a_scale[i] b_scale[j] + bias[j]: the sum an exact
+ * integer (any int8 entries, -128 included), then FP32, rounded once to
+ * out_dtype.  A: m x k int8 (lda >= k), B: n x k int8 (ldb >= k; the n output
+ * channels as rows), bias: n floats or NULL, C: m x n of out_dtype (ldc >= n).
+ * k < 2^17 (else OS2_ERR_UNSUPPORTED); k = 0 gives the bias.  Rows of B on
+ * 16-byte boundaries are fastest. */
+os2_status os2_i8gemm(int m, int n, int k, const int8_t *A, int lda, const float *a_scale,
+                      const int8_t *B, int ldb, const float *b_scale, const float *bias, void *C,
+                      int ldc, int out_dtype, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/* os2_quantize_rows of X (m x k of `dtype`), then os2_i8gemm, in one call: a
+ * linear layer with 8-bit weights whose input is quantised token by token. */
+os2_status os2_i8linear(int m, int n, int k, int dtype, const void *X, int ldx, const int8_t *B,
+                        int ldb, const float *b_scale, const float *bias, void *C, int ldc,
+                        int out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Device workspace of os2_xent (backward = 0) and os2_xent_backward (1): the
+ * packed rows of H and, in the backward pass, one piece of the logits'
+ * gradients (at most 256 MB, or 2048 columns).  0 on bad args; W and ldw as in
+ * the call (their alignment decides; W is not read).  256-byte aligned. */
+size_t os2_xent_workspace_size(int n, int k, int v, const void *W, int ldw, int backward);
+
+/* Softmax cross entropy of the logits z = H W^T, which are never in memory:
+ *   lse[i] = log sum_v exp z_iv,   loss[i] = lse[i] - z_i,labels[i].
+ * H: n x k, W: v x k, both of `dtype` (OS2_F16 or OS2_BF16; OS2_F32 gives
+ * OS2_ERR_UNSUPPORTED), ldh, ldw >= k; labels: n int64.  Rows whose label is
+ * ignore_index have loss 0 and lse 0 and are not computed.  Any other label
+ * outside [0, v) sets OS2_ERR_RANGE in the status word and counts as ignored.
+ * Sums and exponentials are FP32.  k >= 1, v >= 1; n, v <= 2^22, k < 2^24
+ * (else OS2_ERR_UNSUPPORTED). */
+os2_status os2_xent(int n, int k, int v, int dtype, const void *H, int ldh, const void *W, int ldw,
+                    const long long *labels, long long ignore_index, float *loss, float *lse,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Its gradient: with d_iv = grad[i] (exp(z_iv - lse[i]) - [v = labels[i]]),
+ * dH = D W and dW = D^T H, where grad[i] is the gradient of loss[i] and lse what
+ * os2_xent returned.  The logits are computed again, a piece of the vocabulary
+ * at a time; D is rounded to `dtype` (FP16 with a power-of-two scale), sums are
+ * FP32, dH (n x k, lddh >= k) and dW (v x k, lddw >= k) of `dtype`, each rounded
+ * once and overwritten.  dH or dW may be NULL.  Ignored rows have dH = 0 and no
+ * part in dW, whatever H and grad hold there. */
+os2_status os2_xent_backward(int n, int k, int v, int dtype, const void *H, int ldh, const void *W,
+                             int ldw, const long long *labels, long long ignore_index,
+                             const float *lse, const float *grad, void *dH, int lddh, void *dW,
+                             int lddw, void *workspace, size_t workspace_bytes, void *stream);
+
+/* One AdamW step, number `step` >= 1, over `count` contiguous tensors at once
+ * (host arrays of `count` device pointers and element counts, read before the
+ * call returns):
+ *   m <- beta1 m + (1 - beta1) g        v <- beta2 v + (1 - beta2) g^2
+ *   p <- p (1 - lr weight_decay) - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ * params of param_dtype, grads of grad_dtype (os2_dtype), in place.
+ * state_bits 32: exp_avg[i], exp_avg_sq[i] are float arrays and the scale
+ * arrays are not read (may be NULL).  state_bits 8: int8 and uint8 codes with
+ * one float a block of 256 elements in exp_avg_scales[i], exp_avg_sq_scales[i]
+ * (ceil(numel / 256) each), the block's largest magnitude a:
+ *   m = a sgn(c) (|c| / 127)^2,   v = a (c / 255)^4,
+ * re-encoded to the nearest code (of the square and fourth root) after the
+ * update, positive v to code 1 at least.  Codes and scales of zero are the
+ * initial state.  A non-finite gradient makes its element (32-bit) or its block
+ * (8-bit) non-finite, as the formula does.  Tensors whose pointers are all
+ * 16-byte aligned are fastest. */
+os2_status os2_adamw(int count, const long long *numel, void *const *params,
+                     const void *const *grads, void *const *exp_avg, void *const *exp_avg_sq,
+                     float *const *exp_avg_scales, float *const *exp_avg_sq_scales,
+                     int param_dtype, int grad_dtype, int state_bits, double lr, double beta1,
+                     double beta2, double eps, double weight_decay, long long step, void *stream);
+
+/* The values that 8-bit moments stand for (codes and scales as above, for one
+ * tensor or for several laid out on blocks of 256): m and v, numel floats. */
+os2_status os2_adamw_moments(long long numel, const int8_t *exp_avg, const float *exp_avg_scale,
+                             const uint8_t *exp_avg_sq, const float *exp_avg_sq_scale, float *m,
+                             float *v, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,3 +12,5 @@ from .binding import (GEMM_S8_SYNC, GEMM_SIMT, GEMM_TC, GEMM_TC_1SM, GEMM_TC_I8,
                       PROBE_F16_1SM, PROBE_F16_2SM, PROBE_S8_SYNC, set_crt_variant,
                       CRT_TC, CRT_SIMT, CRT_AUTO, scale_bounds, exponents_from_bounds,
                       gemm_exponents)
+from .head import (ADAMW_BLOCK, XentFunction, adamw, adamw_moments, i8gemm, i8linear,  # noqa: F401
+                   quantize_rows, xent, xent_backward)

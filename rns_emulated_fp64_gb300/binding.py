@@ -29,7 +29,10 @@ EXPORTS = ("os2_workspace_size", "os2_gemm", "os2_host_workspace_size", "os2_gem
            "os2_gemm_launch_count", "os2_profile_start", "os2_profile_stop",
            "os2_gemm_noalloc", "os2_sgemm", "os2_complex_workspace_size", "os2_zgemm",
            "os2_cgemm", "os2_wait_selftest", "os2_peak_probe", "os2_set_crt_variant",
-           "os2_scale_bounds", "os2_exponents_from_bounds", "os2_gemm_exponents")
+           "os2_scale_bounds", "os2_exponents_from_bounds", "os2_gemm_exponents",
+           "os2_quantize_rows", "os2_i8gemm_workspace_size", "os2_i8gemm", "os2_i8linear",
+           "os2_xent_workspace_size", "os2_xent", "os2_xent_backward", "os2_adamw",
+           "os2_adamw_moments")
 
 _lib = None
 _lock = threading.Lock()
@@ -112,6 +115,25 @@ def load(build_if_missing: bool = True):
         L.os2_exponents_from_bounds.restype = i
         L.os2_gemm_exponents.argtypes = [i, i, i, d, i, d, i, d, i, i, vp, vp, vp, sz, vp]
         L.os2_gemm_exponents.restype = i
+        q, dbl = ct.c_longlong, ct.c_double
+        L.os2_quantize_rows.argtypes = [i, i, i, d, i, d, i, d, vp]
+        L.os2_quantize_rows.restype = i
+        L.os2_i8gemm_workspace_size.argtypes = [i, i, i, d, i]
+        L.os2_i8gemm_workspace_size.restype = sz
+        L.os2_i8gemm.argtypes = [i, i, i, d, i, d, d, i, d, d, d, i, i, vp, sz, vp]
+        L.os2_i8gemm.restype = i
+        L.os2_i8linear.argtypes = [i, i, i, i, d, i, d, i, d, d, d, i, i, vp, sz, vp]
+        L.os2_i8linear.restype = i
+        L.os2_xent_workspace_size.argtypes = [i, i, i, d, i, i]
+        L.os2_xent_workspace_size.restype = sz
+        L.os2_xent.argtypes = [i, i, i, i, d, i, d, i, d, q, d, d, vp, sz, vp]
+        L.os2_xent.restype = i
+        L.os2_xent_backward.argtypes = [i, i, i, i, d, i, d, i, d, q, d, d, d, i, d, i, vp, sz, vp]
+        L.os2_xent_backward.restype = i
+        L.os2_adamw.argtypes = [i, vp, vp, vp, vp, vp, vp, vp, i, i, i, dbl, dbl, dbl, dbl, dbl, q, vp]
+        L.os2_adamw.restype = i
+        L.os2_adamw_moments.argtypes = [q, d, d, d, d, d, d, vp]
+        L.os2_adamw_moments.restype = i
         _lib = L
         return L
 

@@ -1,0 +1,358 @@
+// Matrix product in 8-bit integers with a scale for each row of A (token) and
+// each row of B (output channel):
+//   y_ij = (sum_h qa_ih qb_jh) sa_i sb_j + bias_j,  the sum an exact int32,
+// and the quantisation it needs:
+//   s_i = max_h |x_ih| / 127,  q_ih = clamp(rint(x_ih / s_i), -127, 127).
+//
+// A few tokens (k_dot): the weights' bytes bound it.  A warp takes rows of B,
+// its lanes 16 bytes apart, four products an instruction (dp4a), every loaded
+// weight used for all tokens at once.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "os2_internal.cuh"
+
+namespace {
+
+template <int DT>
+__device__ __forceinline__ float load_f(const void *p, size_t i) {
+  if (DT == OS2_F32) return static_cast<const float *>(p)[i];
+  if (DT == OS2_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+  return __half2float(static_cast<const __half *>(p)[i]);
+}
+
+// 8 consecutive entries, of which n exist (vec: base and pitch allow 16-byte loads)
+template <int DT>
+__device__ __forceinline__ void load8(const void *p, size_t i, int n, bool vec, float (&x)[8]) {
+  if (vec && n >= 8) {
+    if (DT == OS2_F32) {
+      const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+      const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + 4);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+      x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        if (DT == OS2_BF16) {
+          x[2 * q] = __uint_as_float(w[q] << 16);
+          x[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+        } else {
+          const float2 f = __half22float2(reinterpret_cast<const __half2 &>(w[q]));
+          x[2 * q] = f.x;
+          x[2 * q + 1] = f.y;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; q++) x[q] = q < n ? load_f<DT>(p, i + q) : 0.f;
+  }
+}
+
+// rint(x / s), clamped: the quotient is the correctly rounded one, so that a
+// plain division gives the same integers.
+__device__ __forceinline__ int quant(float x, float s) {
+  return (int)fminf(fmaxf(rintf(__fdiv_rn(x, s)), -127.f), 127.f);
+}
+
+constexpr int kQThreads = 256;
+
+// One CTA a row: the row's largest magnitude, then its integers (the second
+// read comes from cache).  The maximum is taken of the bits of |x|, which order
+// as the values do and put Inf and NaN above every number.  Entries h in [k,
+// kz) are written as zeros.
+template <int DT>
+__global__ void __launch_bounds__(kQThreads)
+    k_quant(int k, const void *X, long ldx, int8_t *q, long ldq, int kz, float *scale, bool vecx,
+            bool vecq) {
+  __shared__ uint32_t s_top[kQThreads / 32];
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const char *x = static_cast<const char *>(X) + (size_t)row * ldx * (DT == OS2_F32 ? 4 : 2);
+  uint32_t top = 0;
+  for (int h = tid * 8; h < k; h += kQThreads * 8) {
+    float v[8];
+    load8<DT>(x, h, k - h, vecx, v);
+#pragma unroll
+    for (int i = 0; i < 8; i++) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((tid & 31) == 0) s_top[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kQThreads / 32; w++) top = max(top, s_top[w]);
+  const bool finite = top < 0x7F800000u;
+  const float s = __fdiv_rn(__uint_as_float(top), 127.f);
+  if (tid == 0) scale[row] = finite ? s : __uint_as_float(0x7FC00000u);
+  int8_t *dst = q + (size_t)row * ldq;
+  for (int h = tid * 8; h < kz; h += kQThreads * 8) {
+    float v[8];
+    load8<DT>(x, h, k - h, vecx, v);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const int c = finite && s > 0.f ? quant(v[i], s) : 0;
+      w[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
+    }
+    if (vecq && h + 8 <= kz) {
+      *reinterpret_cast<uint2 *>(dst + h) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i++)
+        if (h + i < kz) dst[h + i] = (int8_t)(w[i >> 2] >> (8 * (i & 3)));
+    }
+  }
+}
+
+// ------------------------------------------------------------- few tokens
+// Tokens in the workspace: 16 zero bytes, k integers, zeros to `pitch`.
+constexpr int kPad = 16;
+long token_pitch(int k) { return (long)os2_round_up((size_t)k, 16) + 2 * kPad; }
+
+__global__ void k_pack_tokens(int k, const int8_t *A, long lda, int8_t *dst, long pitch) {
+  const int8_t *a = A + (size_t)blockIdx.x * lda;
+  int8_t *d = dst + (size_t)blockIdx.x * pitch;
+  for (int h = threadIdx.x; h < pitch; h += blockDim.x)
+    d[h] = h >= kPad && h - kPad < k ? a[h - kPad] : 0;
+}
+
+template <int OT>
+__device__ __forceinline__ void store_y(void *y, size_t i, float v) {
+  if (OT == OS2_F32) static_cast<float *>(y)[i] = v;
+  else if (OT == OS2_BF16) static_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half *>(y)[i] = __float2half_rn(v);
+}
+
+// The 16 weights of a row at bytes [at, at + 16) of it, those outside [0, k) as 0.
+__device__ __forceinline__ uint4 load_w(const int8_t *row, int at, int k) {
+  if (at >= 0 && at + 16 <= k) return __ldg(reinterpret_cast<const uint4 *>(row + at));
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; i++)
+    if (at + i >= 0 && at + i < k) w[i >> 2] |= (uint32_t)(uint8_t)row[at + i] << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The 16 integers of a token that meet them (t: the token's h = 0).
+template <bool ALIGNED>
+__device__ __forceinline__ uint4 load_t(const int8_t *t, int at) {
+  if (ALIGNED) return __ldg(reinterpret_cast<const uint4 *>(t + at));
+  const uint32_t *w = reinterpret_cast<const uint32_t *>(t + (at & ~3));
+  const int sh = (at & 3) * 8;
+  uint32_t r[5];
+#pragma unroll
+  for (int i = 0; i < 5; i++) r[i] = __ldg(w + i);
+  return make_uint4(__funnelshift_r(r[0], r[1], sh), __funnelshift_r(r[1], r[2], sh),
+                    __funnelshift_r(r[2], r[3], sh), __funnelshift_r(r[3], r[4], sh));
+}
+
+constexpr int kDotThreads = 256;
+
+// M tokens at once (the last group of a call may have fewer), R rows of B a
+// warp, U loads of 16 bytes a lane and row in flight.  Rows of B that start off
+// a 16-byte boundary (ALIGNED false) are read in aligned pieces all the same,
+// and the tokens shifted against them.
+template <int M, int R, int U, bool ALIGNED, int OT>
+__global__ void __launch_bounds__(kDotThreads)
+    k_dot(int m, int n, int k, const int8_t *T, long pitch, const float *sa, const int8_t *B,
+          long ldb, const float *sb, const float *bias, void *C, long ldc) {
+  const int lane = threadIdx.x & 31;
+  const int warps = gridDim.x * (kDotThreads / 32);
+  const int groups = (n + R - 1) / R;
+  for (int g = blockIdx.x * (kDotThreads / 32) + (threadIdx.x >> 5); g < groups; g += warps) {
+    int acc[R][M];
+    const int8_t *row[R];
+    int off[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      row[r] = B + (size_t)min(g * R + r, n - 1) * ldb;  // a row past the end: the last again
+      off[r] = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(row[r]) & 15);
+#pragma unroll
+      for (int t = 0; t < M; t++) acc[r][t] = 0;
+    }
+    const int end = ALIGNED ? k : k + 15;  // pieces of 16 that meet [0, k) at any offset
+    for (int h = lane * 16; h < end; h += 512 * U) {
+      uint4 w[R][U];
+#pragma unroll
+      for (int u = 0; u < U; u++)
+#pragma unroll
+        for (int r = 0; r < R; r++)
+          w[r][u] = h + 512 * u < k + off[r] ? load_w(row[r], h + 512 * u - off[r], k)
+                                             : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        if (h + 512 * u >= end) break;
+#pragma unroll
+        for (int t = 0; t < M; t++) {
+          if (t >= m) break;
+          const int8_t *tok = T + (size_t)t * pitch + kPad;
+          uint4 x;
+          if (ALIGNED) x = load_t<true>(tok, h + 512 * u);
+#pragma unroll
+          for (int r = 0; r < R; r++) {
+            // a piece wholly past the row holds zeros; its tokens are not read
+            if (!ALIGNED) x = load_t<false>(tok, min(h + 512 * u - off[r], k - 1));
+            int a = acc[r][t];
+            a = __dp4a((int)w[r][u].x, (int)x.x, a);
+            a = __dp4a((int)w[r][u].y, (int)x.y, a);
+            a = __dp4a((int)w[r][u].z, (int)x.z, a);
+            a = __dp4a((int)w[r][u].w, (int)x.w, a);
+            acc[r][t] = a;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; r++)
+#pragma unroll
+      for (int t = 0; t < M; t++) {
+        const int sum = __reduce_add_sync(0xffffffffu, acc[r][t]);
+        const int j = g * R + r;
+        if (lane == r * M + t && t < m && j < n) {
+          const float y = (float)sum * sa[t] * sb[j];
+          store_y<OT>(C, (size_t)t * ldc + j, bias ? y + bias[j] : y);
+        }
+      }
+  }
+}
+
+template <int M, int R, int U, bool ALIGNED>
+void launch_dot_o(int ot, int m, int n, int k, const int8_t *T, long pitch, const float *sa,
+                  const int8_t *B, long ldb, const float *sb, const float *bias, void *C, long ldc,
+                  cudaStream_t s) {
+  const int groups = (n + R - 1) / R, per = kDotThreads / 32;
+  const int grid = std::min((groups + per - 1) / per, 8 * os2_sm_count());
+  if (ot == OS2_F32)
+    k_dot<M, R, U, ALIGNED, OS2_F32><<<grid, kDotThreads, 0, s>>>(m, n, k, T, pitch, sa, B, ldb, sb, bias, C, ldc);
+  else if (ot == OS2_BF16)
+    k_dot<M, R, U, ALIGNED, OS2_BF16><<<grid, kDotThreads, 0, s>>>(m, n, k, T, pitch, sa, B, ldb, sb, bias, C, ldc);
+  else
+    k_dot<M, R, U, ALIGNED, OS2_F16><<<grid, kDotThreads, 0, s>>>(m, n, k, T, pitch, sa, B, ldb, sb, bias, C, ldc);
+}
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t elem_size(int dt) { return dt == OS2_F32 ? 4 : 2; }
+bool is_dtype(int dt) { return dt == OS2_F32 || dt == OS2_F16 || dt == OS2_BF16; }
+
+constexpr int kDotTokens = 8;
+
+cudaError_t dot(int ot, int m, int n, int k, const int8_t *T, long pitch, const float *sa,
+                const int8_t *B, long ldb, const float *sb, const float *bias, void *C, long ldc,
+                cudaStream_t s) {
+  const bool al = aligned(B, 16) && ldb % 16 == 0;
+  for (int t0 = 0; t0 < m; t0 += kDotTokens) {
+    const int mt = std::min(kDotTokens, m - t0);
+    const int8_t *Tt = T + (size_t)t0 * pitch;
+    void *Ct = static_cast<char *>(C) + (size_t)t0 * ldc * elem_size(ot);
+#define DOT(M, R, U)                                                                              \
+  (al ? launch_dot_o<M, R, U, true>(ot, mt, n, k, Tt, pitch, sa + t0, B, ldb, sb, bias, Ct, ldc, s) \
+      : launch_dot_o<M, R, U, false>(ot, mt, n, k, Tt, pitch, sa + t0, B, ldb, sb, bias, Ct, ldc, s))
+    if (mt == 1) DOT(1, 1, 4);
+    else if (mt <= 4) DOT(4, 2, 2);
+    else DOT(8, 4, 1);
+#undef DOT
+  }
+  return cudaGetLastError();
+}
+
+struct Layout {
+  size_t tokens, scale, total;
+};
+Layout layout(int m, int k) {
+  Layout L;
+  L.tokens = 0;
+  L.scale = os2_round_up((size_t)m * token_pitch(k), 256);
+  L.total = L.scale + os2_round_up((size_t)m * 4, 256);
+  return L;
+}
+
+cudaError_t quantize(int m, int k, int dtype, const void *X, long ldx, int8_t *q, long ldq, int kz,
+                     float *scale, cudaStream_t s) {
+  const bool vecx = aligned(X, 16) && (ldx * elem_size(dtype)) % 16 == 0;
+  const bool vecq = aligned(q, 8) && ldq % 8 == 0;
+  if (dtype == OS2_F32)
+    k_quant<OS2_F32><<<m, kQThreads, 0, s>>>(k, X, ldx, q, ldq, kz, scale, vecx, vecq);
+  else if (dtype == OS2_BF16)
+    k_quant<OS2_BF16><<<m, kQThreads, 0, s>>>(k, X, ldx, q, ldq, kz, scale, vecx, vecq);
+  else
+    k_quant<OS2_F16><<<m, kQThreads, 0, s>>>(k, X, ldx, q, ldq, kz, scale, vecx, vecq);
+  return cudaGetLastError();
+}
+
+// |sum| <= k 2^14 stays below 2^31
+constexpr int kMaxK = (1 << 17) - 1;
+constexpr int kMaxDim = 1 << 24;
+
+os2_status check(int m, int n, int k, const void *A, int lda, const void *B, int ldb,
+                 const float *sb, const float *bias, const void *C, int ldc, int ot) {
+  if (m < 0 || n < 0 || k < 0 || lda < k || ldb < k || ldc < n || !is_dtype(ot))
+    return OS2_ERR_INVALID_ARG;
+  if (m > 0 && n > 0 && (!C || !aligned(C, elem_size(ot)) || !sb || !aligned(sb, 4) ||
+                         (bias && !aligned(bias, 4)) || (k > 0 && (!A || !B))))
+    return OS2_ERR_INVALID_ARG;
+  if (k > kMaxK || m > kMaxDim || n > kMaxDim) return OS2_ERR_UNSUPPORTED;
+  return OS2_OK;
+}
+
+}  // namespace
+
+extern "C" os2_status os2_quantize_rows(int m, int k, int dtype, const void *X, int ldx, int8_t *q,
+                                        int ldq, float *scale, void *stream) {
+  if (m < 0 || k < 0 || ldx < k || ldq < k || !is_dtype(dtype)) return OS2_ERR_INVALID_ARG;
+  if (m == 0) return OS2_OK;
+  if (!scale || !aligned(scale, 4) || (k > 0 && (!X || !q || !aligned(X, elem_size(dtype)))))
+    return OS2_ERR_INVALID_ARG;
+  return quantize(m, k, dtype, X, ldx, q, ldq, k, scale, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? OS2_OK
+             : OS2_ERR_CUDA;
+}
+
+extern "C" size_t os2_i8gemm_workspace_size(int m, int n, int k, const void *B, int ldb) {
+  if (m < 0 || n < 0 || k < 0 || k > kMaxK || m > kMaxDim || n > kMaxDim || ldb < k) return 0;
+  return layout(m, k).total;
+}
+
+extern "C" os2_status os2_i8gemm(int m, int n, int k, const int8_t *A, int lda,
+                                 const float *a_scale, const int8_t *B, int ldb,
+                                 const float *b_scale, const float *bias, void *C, int ldc,
+                                 int out_dtype, void *workspace, size_t workspace_bytes,
+                                 void *stream) {
+  const os2_status st = check(m, n, k, A, lda, B, ldb, b_scale, bias, C, ldc, out_dtype);
+  if (st) return st;
+  if (m == 0 || n == 0) return OS2_OK;
+  if (!a_scale || !aligned(a_scale, 4)) return OS2_ERR_INVALID_ARG;
+  const Layout L = layout(m, k);
+  if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256))
+    return OS2_ERR_WORKSPACE;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int8_t *T = static_cast<int8_t *>(workspace) + L.tokens;
+  k_pack_tokens<<<m, 256, 0, s>>>(k, A, lda, T, token_pitch(k));
+  return dot(out_dtype, m, n, k, T, token_pitch(k), a_scale, B, ldb, b_scale, bias, C, ldc, s) ==
+                 cudaSuccess
+             ? OS2_OK
+             : OS2_ERR_CUDA;
+}
+
+extern "C" os2_status os2_i8linear(int m, int n, int k, int dtype, const void *X, int ldx,
+                                   const int8_t *B, int ldb, const float *b_scale,
+                                   const float *bias, void *C, int ldc, int out_dtype,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
+  if (!is_dtype(dtype) || (X && !aligned(X, elem_size(dtype)))) return OS2_ERR_INVALID_ARG;
+  const os2_status st = check(m, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, out_dtype);
+  if (st) return st;
+  if (m == 0 || n == 0) return OS2_OK;
+  const Layout L = layout(m, k);
+  if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256))
+    return OS2_ERR_WORKSPACE;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int8_t *T = static_cast<int8_t *>(workspace) + L.tokens;
+  float *sa = reinterpret_cast<float *>(static_cast<char *>(workspace) + L.scale);
+  const long pitch = token_pitch(k);
+  cudaError_t e = quantize(m, k, dtype, X, ldx, T + kPad, pitch, (int)(pitch - 2 * kPad), sa, s);
+  if (e == cudaSuccess)
+    e = dot(out_dtype, m, n, k, T, pitch, sa, B, ldb, b_scale, bias, C, ldc, s);
+  return e == cudaSuccess ? OS2_OK : OS2_ERR_CUDA;
+}

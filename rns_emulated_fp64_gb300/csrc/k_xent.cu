@@ -1,0 +1,619 @@
+// Softmax cross entropy of a vocabulary head, z = H W^T, with its gradient,
+// without the logits in memory.
+//
+//   forward   lse_i = log sum_v exp z_iv,  loss_i = lse_i - z_i,y(i)
+//   backward  d_iv = g_i (exp(z_iv - lse_i) - [v = y_i]),  dH = D W,  dW = D^T H
+//
+// Rows whose label is the ignored one are taken out first: k_xent_prep packs
+// the rows that count into the workspace (their number stays on the device),
+// so they cost no products, and what they hold (Inf, NaN) reaches nothing.
+// Forward: one product (mm2.cuh) whose epilogue keeps each row's running
+// maximum and sum over 128 columns and writes that pair; a second kernel joins
+// a row's pairs in their order.  Backward, for each piece of the vocabulary:
+// the logits' product again, whose epilogue writes D in the operands' type,
+// then D W (added in FP32 over the pieces) and D^T H, which take W, D and H as
+// they lie (MN-major operands: nothing is transposed in memory).
+// The tensor cores bound all three products for more than some 300 rows (2 n
+// flop a byte of W), the weights' bytes below that.
+#include "mm2.cuh"
+
+using namespace os2mm;
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return reinterpret_cast<const uint32_t &>(v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return reinterpret_cast<const uint32_t &>(v);
+}
+template <bool BF16>
+__device__ __forceinline__ uint16_t pack1(float a) {
+  return (uint16_t)(pack2<BF16>(a, 0.f) & 0xFFFFu);
+}
+
+// ------------------------------------------------------------ rows that count
+struct Prep {
+  int n, k, v;
+  const uint16_t *H;
+  long ldh;
+  const long long *labels;
+  long long ignore;
+  int rows_cta;          // rows of H a CTA takes
+  // packed
+  int *count;            // rows that count
+  int *rowmap, *label;   // [n]
+  uint16_t *Hc;          // [npad][kp]
+  long kp, npad;
+  // forward
+  float *loss, *lse;     // zeroed for the others
+  // backward
+  const float *lse_in, *grad;
+  float *lse_c, *grad_c; // [n]
+  float *scale;          // {log2 c, 1 / c}
+  bool f16;
+  uint16_t *dH;          // zeroed for the others (may be null)
+  long lddh;
+  int *status;
+};
+
+__device__ __forceinline__ bool counts(long long y, const Prep &p) {
+  return y != p.ignore && y >= 0 && y < p.v;
+}
+
+// Each CTA counts the labels before its rows for itself (n labels from L2; a
+// few microseconds at most beside a product over the rows), so packing takes
+// one launch.
+constexpr int kPrepThreads = 256;
+__global__ void __launch_bounds__(kPrepThreads) k_xent_prep(const Prep p) {
+  __shared__ int s_sum[2];
+  __shared__ float s_max[kPrepThreads / 32];
+  __shared__ int s_pos[kPrepThreads], s_warp[kPrepThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r0 = blockIdx.x * p.rows_cta, r1 = min(p.n, r0 + p.rows_cta);
+  if (tid < 2) s_sum[tid] = 0;
+  __syncthreads();
+  int before = 0, total = 0;
+  float gmax = 0.f;
+  for (int i = tid; i < p.n; i += kPrepThreads) {
+    const bool c = counts(p.labels[i], p);
+    total += c;
+    before += c && i < r0;
+    if (p.grad && c && blockIdx.x == 0) gmax = fmaxf(gmax, fabsf(p.grad[i]));
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if (lane == 0) {
+    atomicAdd(&s_sum[0], before);
+    atomicAdd(&s_sum[1], total);
+  }
+  if (p.grad && blockIdx.x == 0) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) gmax = fmaxf(gmax, __shfl_xor_sync(0xffffffffu, gmax, o));
+    if (lane == 0) s_max[warp] = gmax;
+  }
+  __syncthreads();
+  int base = s_sum[0];
+  const int nv = s_sum[1];
+  if (blockIdx.x == 0 && tid == 0) {
+    *p.count = nv;
+    if (p.grad) {
+      // The logits' gradients are held times c = 2^e, which puts the largest |g|
+      // (|d| <= |g|) below 2^14 in FP16 and 2^41 in BF16: a probability keeps its
+      // full precision down to 2^-28 and 2^-160, and vanishes below 2^-38 and
+      // 2^-174.
+      const int want = p.f16 ? 13 : 40;
+      int e = want;
+      float g = 0.f;
+      for (int w = 0; w < kPrepThreads / 32; w++) g = fmaxf(g, s_max[w]);
+      if (g > 0.f && g < INFINITY) e = min(max(want - ilogbf(g), -100), 100);
+      p.scale[0] = (float)e;
+      p.scale[1] = exp2f((float)-e);
+    }
+  }
+  const bool vec = (p.ldh % 8 == 0) && (reinterpret_cast<uintptr_t>(p.H) % 16 == 0);
+  for (int c0 = r0; c0 < r1; c0 += kPrepThreads) {
+    const int i = c0 + tid;
+    const long long y = i < r1 ? p.labels[i] : p.ignore;
+    const bool c = i < r1 && counts(y, p);
+    if (i < r1 && !c && y != p.ignore) set_status(p.status, OS2_ERR_RANGE);
+    const unsigned b = __ballot_sync(0xffffffffu, c);
+    if (lane == 0) s_warp[warp] = __popc(b);
+    __syncthreads();
+    int pos = base + __popc(b & ((1u << lane) - 1));
+    int all = 0;
+    for (int w = 0; w < kPrepThreads / 32; w++) {
+      pos += w < warp ? s_warp[w] : 0;
+      all += s_warp[w];
+    }
+    s_pos[tid] = c ? pos : -1;
+    if (c && OS2_DBG_GUARD(pos >= 0 && pos < p.n, p.status)) {
+      p.rowmap[pos] = i;
+      p.label[pos] = (int)y;
+      if (p.grad) {
+        p.lse_c[pos] = p.lse_in[i];
+        p.grad_c[pos] = p.grad[i];
+      }
+    } else if (i < r1 && p.loss) {
+      p.loss[i] = 0.f;
+      p.lse[i] = 0.f;
+    }
+    __syncthreads();
+    const int rows = min(kPrepThreads, r1 - c0);
+    for (int r = warp; r < rows; r += kPrepThreads / 32) {
+      const int at = s_pos[r];
+      if (at >= 0 && OS2_DBG_GUARD(at < p.npad && p.k <= p.kp, p.status)) {
+        const uint16_t *src = p.H + (size_t)(c0 + r) * p.ldh;
+        uint16_t *dst = p.Hc + (size_t)at * p.kp;
+        int h = 0;
+        if (vec) {
+          for (h = lane * 8; h + 8 <= p.k; h += 256)
+            *reinterpret_cast<uint4 *>(dst + h) = *reinterpret_cast<const uint4 *>(src + h);
+          h = p.k / 8 * 8;
+        }
+        for (h += lane; h < p.k; h += 32) dst[h] = src[h];
+      } else if (at < 0 && p.dH) {
+        uint16_t *dst = p.dH + (size_t)(c0 + r) * p.lddh;
+        for (int h = lane; h < p.k; h += 32) dst[h] = 0;
+      }
+    }
+    base += all;
+    __syncthreads();
+  }
+  // the last stage's rows past the count take part in D^T H: zeros
+  const int end = (int)min((long)(nv + kStageK - 1) / kStageK * kStageK, p.npad);
+  for (int r = nv + blockIdx.x * (kPrepThreads / 32) + warp; r < end;
+       r += gridDim.x * (kPrepThreads / 32))
+    for (long h = lane * 8; h < p.kp; h += 256)
+      *reinterpret_cast<uint4 *>(p.Hc + (size_t)r * p.kp + h) = make_uint4(0, 0, 0, 0);
+}
+
+// W's rows at a pitch and base that TMA takes (only where W's own are not)
+__global__ void k_repack(const uint16_t *src, long ld, uint16_t *dst, long pitch, int rows, int k) {
+  for (long r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int h = threadIdx.x; h < k; h += blockDim.x) dst[r * pitch + h] = src[r * ld + h];
+}
+
+// ------------------------------------------------------------ epilogues
+// Forward: maximum (times log2 e) and sum of exponentials of 128 columns.
+struct StatsEpi {
+  const int *label;
+  float *zlabel;
+  float2 *part;   // [rows][parts]
+  int parts, v;
+
+  __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, int, int m,
+                                       int *status) {
+    const int y = row < m ? label[row] - col0 : -1;
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+    for (int g = 0; g < 4; g++) {
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld32(taddr + g * 32, r);
+      tmem_wait_ld();
+      const int left = v - (col0 + g * 32);  // columns of this group that exist
+      if (left <= 0) break;
+      if (left < 32) {
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+          if (i >= left) r[i] = 0xFF800000u;  // -inf
+      }
+      float mx = __uint_as_float(r[0]);
+#pragma unroll
+      for (int i = 1; i < 32; i++) mx = fmaxf(mx, __uint_as_float(r[i]));
+      const float t = fmaxf(top, mx * kLog2e);
+      // a row of -inf so far: exponents against 0 (every term is 0)
+      const float t0 = t == -INFINITY ? 0.f : t;
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        s0 += ex2(fmaf(__uint_as_float(r[i]), kLog2e, -t0));
+        s1 += ex2(fmaf(__uint_as_float(r[i + 1]), kLog2e, -t0));
+      }
+      sum = sum * ex2(top - t0) + (s0 + s1);
+      top = t;
+      if ((unsigned)(y - g * 32) < 32u) {
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+          if (i == y - g * 32) z = __uint_as_float(r[i]);
+        zlabel[row] = z;
+      }
+    }
+    if (row < m && OS2_DBG_GUARD((col0 >> 7) < parts, status))
+      part[(size_t)row * parts + (col0 >> 7)] = make_float2(top, sum);
+  }
+};
+
+// Backward: D of one piece (columns v0 .. v0 + v) in the operands' type.  Its
+// rounding is that of one operand of a product whose sums are FP32, as H's and
+// W's own roundings are.  Rows and columns past the ends are zeros: they are
+// terms of the next products.
+template <bool BF16>
+struct GradEpi {
+  const int *label;
+  const float *lse, *grad, *scale;
+  uint16_t *d;
+  long pitch;     // multiple of 256
+  int v0, v;
+
+  __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, int, int m, int *) {
+    const bool in = row < m;
+    const int y = in ? label[row] - v0 - col0 : -1;
+    // c p = 2^(z log2 e - lse log2 e + log2 c): below FP32's range only with c in it
+    const float e = scale[0], c = exp2f(e);
+    const float l = in ? fmaf(lse[row], kLog2e, -e) : 0.f, gr = in ? grad[row] : 0.f;
+    uint4 *dst = reinterpret_cast<uint4 *>(d + (size_t)row * pitch + col0);
+#pragma unroll 1
+    for (int g = 0; g < 4; g++) {
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld32(taddr + g * 32, r);
+      tmem_wait_ld();
+      const int left = v - (col0 + g * 32), yg = y - g * 32;
+      float x[32];
+#pragma unroll
+      for (int i = 0; i < 32; i++) x[i] = ex2(fmaf(__uint_as_float(r[i]), kLog2e, -l));
+      if ((unsigned)yg < 32u) {
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+          if (i == yg) x[i] -= c;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i++) x[i] = (in && i < left) ? x[i] * gr : 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; q++)
+        dst[g * 4 + q] = make_uint4(pack2<BF16>(x[8 * q], x[8 * q + 1]),
+                                    pack2<BF16>(x[8 * q + 2], x[8 * q + 3]),
+                                    pack2<BF16>(x[8 * q + 4], x[8 * q + 5]),
+                                    pack2<BF16>(x[8 * q + 6], x[8 * q + 7]));
+    }
+  }
+};
+
+// dH and dW: times 1 / c, rounded once, to the row that a packed row came from;
+// dH's sums over the pieces stay in FP32 until the last.
+template <bool BF16>
+struct StoreEpi {
+  uint16_t *out;
+  long ld;
+  const int *rowmap;    // or null
+  const float *scale;
+  float *acc;           // [rows][acc_pitch], acc_pitch a multiple of 256; null with one piece
+  long acc_pitch;
+  int first, last, n;
+  bool vec;             // rows of `out` are 16-byte aligned
+
+  __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, int, int m, int *) {
+    const bool in = row < m;
+    const float s = scale[1];
+    uint16_t *dst = nullptr;
+    if (in && last) dst = out + (size_t)(rowmap ? rowmap[row] : row) * ld + col0;
+    float4 *a = acc && in ? reinterpret_cast<float4 *>(acc + (size_t)row * acc_pitch + col0) : nullptr;
+#pragma unroll 1
+    for (int g = 0; g < 4; g++) {
+      float4 av[8];
+      if (a && !first) {
+#pragma unroll
+        for (int q = 0; q < 8; q++) av[q] = a[g * 8 + q];
+      }
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld32(taddr + g * 32, r);
+      tmem_wait_ld();
+      float x[32];
+#pragma unroll
+      for (int i = 0; i < 32; i++) x[i] = __uint_as_float(r[i]);
+      if (a && !first) {
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
+          x[4 * q] += av[q].x;
+          x[4 * q + 1] += av[q].y;
+          x[4 * q + 2] += av[q].z;
+          x[4 * q + 3] += av[q].w;
+        }
+      }
+      if (!in) continue;
+      if (!last) {
+#pragma unroll
+        for (int q = 0; q < 8; q++)
+          a[g * 8 + q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+        continue;
+      }
+      const int left = n - (col0 + g * 32);
+      if (left >= 32 && vec) {
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+          reinterpret_cast<uint4 *>(dst + g * 32)[q] =
+              make_uint4(pack2<BF16>(x[8 * q] * s, x[8 * q + 1] * s),
+                         pack2<BF16>(x[8 * q + 2] * s, x[8 * q + 3] * s),
+                         pack2<BF16>(x[8 * q + 4] * s, x[8 * q + 5] * s),
+                         pack2<BF16>(x[8 * q + 6] * s, x[8 * q + 7] * s));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+          if (i < left) dst[g * 32 + i] = pack1<BF16>(x[i] * s);
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------ joining a row
+__global__ void __launch_bounds__(256)
+    k_xent_join(const int *count, const int *rowmap, const float *zlabel, const float2 *part,
+                int parts, float *loss, float *lse) {
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= *count) return;
+  const float2 *p = part + (size_t)row * parts;
+  float top = -INFINITY, sum = 0.f;
+  for (int i = lane; i < parts; i += 32) {
+    const float2 v = p[i];
+    const float t = fmaxf(top, v.x), t0 = t == -INFINITY ? 0.f : t;
+    sum = sum * ex2(top - t0) + v.y * ex2(v.x - t0);
+    top = t;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, top, o), y = __shfl_xor_sync(0xffffffffu, sum, o);
+    const float t = fmaxf(top, x), t0 = t == -INFINITY ? 0.f : t;
+    sum = sum * ex2(top - t0) + y * ex2(x - t0);
+    top = t;
+  }
+  if (lane == 0) {
+    const float l = top * kLn2 + logf(sum);
+    const int to = rowmap[row];
+    lse[to] = l;
+    loss[to] = l - zlabel[row];
+  }
+}
+
+// ------------------------------------------------------------------- host --
+bool tma_rows(const void *p, long ld) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0;
+}
+
+// D's piece of the vocabulary: at most 2^27 entries (256 MB) of packed rows x
+// columns, at least 2048 columns, pieces of equal size.  Larger pieces read and
+// write dH's FP32 sums less often; D leaves L2 either way.
+int piece_columns(long npad, int v) {
+  const long most = std::max<long>((1L << 27) / npad / 256 * 256, 2048);
+  const long pieces = (v + most - 1) / most;
+  return (int)os2_round_up((size_t)((v + pieces - 1) / pieces), 256);
+}
+
+struct Layout {
+  long npad, kp;
+  int parts, vc, pieces;
+  size_t count, rowmap, label, zlabel, part, Hc, Wc, lse_c, grad_c, scale, d, acc, total;
+};
+
+Layout layout(int n, int k, int v, const void *W, int ldw, bool backward) {
+  Layout L = {};
+  L.npad = (long)os2_round_up((size_t)n, 256);
+  L.kp = (long)os2_round_up((size_t)k, 64);
+  L.parts = (v + kBN - 1) / kBN * 2;
+  L.vc = piece_columns(std::max(L.npad, 256L), v);
+  L.pieces = (v + L.vc - 1) / L.vc;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += os2_round_up(bytes, 256);
+    return o;
+  };
+  L.count = take(4);
+  L.rowmap = take((size_t)n * 4);
+  L.label = take((size_t)n * 4);
+  L.Hc = take((size_t)L.npad * L.kp * 2);
+  if (!tma_rows(W, ldw)) L.Wc = take((size_t)v * L.kp * 2);
+  if (backward) {
+    L.lse_c = take((size_t)n * 4);
+    L.grad_c = take((size_t)n * 4);
+    L.scale = take(8);
+    L.d = take((size_t)L.npad * L.vc * 2);
+    if (L.pieces > 1) L.acc = take((size_t)L.npad * os2_round_up((size_t)k, 256) * 4);
+  } else {
+    L.zlabel = take((size_t)n * 4);
+    L.part = take((size_t)n * L.parts * 8);
+  }
+  L.total = at;
+  return L;
+}
+
+template <class T>
+T *at(void *ws, size_t off) {
+  return reinterpret_cast<T *>(static_cast<char *>(ws) + off);
+}
+
+// Packs the rows, and W where TMA cannot take it as it lies (W, ldw: in, out).
+cudaError_t prepare(const Layout &L, Prep &p, const uint16_t *&W, long &ldw, void *ws,
+                    cudaStream_t s) {
+  p.count = at<int>(ws, L.count);
+  p.rowmap = at<int>(ws, L.rowmap);
+  p.label = at<int>(ws, L.label);
+  p.Hc = at<uint16_t>(ws, L.Hc);
+  p.kp = L.kp;
+  p.npad = L.npad;
+  p.rows_cta = std::max(8, (p.n + 4 * os2_sm_count() - 1) / (4 * os2_sm_count()));
+  k_xent_prep<<<(p.n + p.rows_cta - 1) / p.rows_cta, kPrepThreads, 0, s>>>(p);
+  if (!tma_rows(W, ldw)) {
+    uint16_t *wc = at<uint16_t>(ws, L.Wc);
+    k_repack<<<std::min(p.v, 8 * os2_sm_count()), 256, 0, s>>>(W, ldw, wc, L.kp, p.v, p.k);
+    W = wc;
+    ldw = L.kp;
+  }
+  return cudaGetLastError();
+}
+
+template <bool BF16>
+cudaError_t forward(Prep p, const uint16_t *W, long ldw, void *ws, const Layout &L,
+                    cudaStream_t s) {
+  cudaError_t e = prepare(L, p, W, ldw, ws, s);
+  if (e != cudaSuccess) return e;
+  CUtensorMap mh, mw;
+  if (!make_map(&mh, p.Hc, BF16, p.k, p.n, L.kp, false) ||
+      !make_map(&mw, W, BF16, p.k, p.v, ldw, false))
+    return cudaErrorInvalidValue;
+  const StatsEpi epi{p.label, at<float>(ws, L.zlabel), at<float2>(ws, L.part), L.parts, p.v};
+  const Job job{p.n, p.v, p.k, p.count, nullptr, INT_MAX};
+  e = launch_mm2<BF16, false, false>(mh, mw, job, epi, p.status, s);
+  if (e != cudaSuccess) return e;
+  k_xent_join<<<(p.n + 7) / 8, 256, 0, s>>>(p.count, p.rowmap, epi.zlabel, epi.part, L.parts,
+                                            p.loss, p.lse);
+  return cudaGetLastError();
+}
+
+template <bool BF16>
+cudaError_t backward(Prep p, const uint16_t *W, long ldw, uint16_t *dW, long lddw, void *ws,
+                     const Layout &L, cudaStream_t s) {
+  p.lse_c = at<float>(ws, L.lse_c);
+  p.grad_c = at<float>(ws, L.grad_c);
+  p.scale = at<float>(ws, L.scale);
+  cudaError_t e = prepare(L, p, W, ldw, ws, s);
+  if (e != cudaSuccess) return e;
+  uint16_t *d = at<uint16_t>(ws, L.d);
+  float *acc = L.pieces > 1 ? at<float>(ws, L.acc) : nullptr;
+  const long acc_pitch = (long)os2_round_up((size_t)p.k, 256);
+  CUtensorMap mh, mht, mw, mwt, md, mdt;
+  if (!make_map(&mh, p.Hc, BF16, p.k, p.n, L.kp, false) ||
+      !make_map(&mht, p.Hc, BF16, p.k, L.npad, L.kp, true))
+    return cudaErrorInvalidValue;
+  for (int i = 0; i < L.pieces; i++) {
+    const int v0 = i * L.vc, vn = std::min(L.vc, p.v - v0);
+    const uint16_t *Wi = W + (size_t)v0 * ldw;
+    if (!make_map(&mw, Wi, BF16, p.k, vn, ldw, false) ||
+        !make_map(&mwt, Wi, BF16, p.k, vn, ldw, true) ||
+        !make_map(&md, d, BF16, L.vc, L.npad, L.vc, false) ||
+        !make_map(&mdt, d, BF16, L.vc, L.npad, L.vc, true))
+      return cudaErrorInvalidValue;
+    const GradEpi<BF16> ge{p.label, p.lse_c, p.grad_c, p.scale, d, L.vc, v0, vn};
+    e = launch_mm2<BF16, false, false>(mh, mw, Job{p.n, vn, p.k, p.count, nullptr, INT_MAX}, ge,
+                                       p.status, s);
+    if (e != cudaSuccess) return e;
+    if (p.dH) {
+      const StoreEpi<BF16> se{p.dH, p.lddh, p.rowmap, p.scale, acc, acc_pitch, i == 0,
+                              i == L.pieces - 1, p.k, tma_rows(p.dH, p.lddh)};
+      e = launch_mm2<BF16, false, true>(md, mwt, Job{p.n, p.k, vn, p.count, nullptr, INT_MAX}, se,
+                                        p.status, s);
+      if (e != cudaSuccess) return e;
+    }
+    if (dW) {
+      const StoreEpi<BF16> se{dW + (size_t)v0 * lddw, lddw, nullptr, p.scale, nullptr, 0, 1, 1,
+                              p.k, tma_rows(dW, lddw)};
+      e = launch_mm2<BF16, true, true>(mdt, mht, Job{vn, p.k, p.n, nullptr, p.count, INT_MAX}, se,
+                                       p.status, s);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
+}
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+constexpr int kMaxRows = 1 << 22;
+
+os2_status check(int n, int k, int v, int dtype, const void *H, int ldh, const void *W, int ldw,
+                 const long long *labels) {
+  if (n < 0 || k < 1 || v < 1 || ldh < k || ldw < k) return OS2_ERR_INVALID_ARG;
+  if (dtype != OS2_F32 && dtype != OS2_F16 && dtype != OS2_BF16) return OS2_ERR_INVALID_ARG;
+  if (!W || !aligned(W, 2)) return OS2_ERR_INVALID_ARG;
+  if (n > 0 && (!H || !labels || !aligned(H, 2) || !aligned(labels, 8))) return OS2_ERR_INVALID_ARG;
+  if (dtype == OS2_F32) return OS2_ERR_UNSUPPORTED;
+  if (n > kMaxRows || v > kMaxRows || k >= (1 << 24)) return OS2_ERR_UNSUPPORTED;
+  return OS2_OK;
+}
+
+}  // namespace
+
+extern "C" size_t os2_xent_workspace_size(int n, int k, int v, const void *W, int ldw,
+                                          int backward) {
+  if (n < 0 || k < 1 || v < 1 || ldw < k || n > kMaxRows || v > kMaxRows || k >= (1 << 24))
+    return 0;
+  return layout(n, k, v, W, ldw, backward != 0).total;
+}
+
+extern "C" os2_status os2_xent(int n, int k, int v, int dtype, const void *H, int ldh,
+                               const void *W, int ldw, const long long *labels,
+                               long long ignore_index, float *loss, float *lse, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+  const os2_status st = check(n, k, v, dtype, H, ldh, W, ldw, labels);
+  if (st) return st;
+  if (n == 0) return OS2_OK;
+  if (!loss || !lse || !aligned(loss, 4) || !aligned(lse, 4)) return OS2_ERR_INVALID_ARG;
+  const Layout L = layout(n, k, v, W, ldw, false);
+  if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256))
+    return OS2_ERR_WORKSPACE;
+  Prep p = {};
+  p.status = os2_status_ptr();
+  if (!p.status) return OS2_ERR_CUDA;
+  p.n = n;
+  p.k = k;
+  p.v = v;
+  p.H = static_cast<const uint16_t *>(H);
+  p.ldh = ldh;
+  p.labels = labels;
+  p.ignore = ignore_index;
+  p.loss = loss;
+  p.lse = lse;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const uint16_t *w = static_cast<const uint16_t *>(W);
+  const cudaError_t e = dtype == OS2_BF16 ? forward<true>(p, w, ldw, workspace, L, s)
+                                          : forward<false>(p, w, ldw, workspace, L, s);
+  return e == cudaSuccess ? OS2_OK : OS2_ERR_CUDA;
+}
+
+extern "C" os2_status os2_xent_backward(int n, int k, int v, int dtype, const void *H, int ldh,
+                                        const void *W, int ldw, const long long *labels,
+                                        long long ignore_index, const float *lse,
+                                        const float *grad, void *dH, int lddh, void *dW, int lddw,
+                                        void *workspace, size_t workspace_bytes, void *stream) {
+  const os2_status st = check(n, k, v, dtype, H, ldh, W, ldw, labels);
+  if (st) return st;
+  if ((dH && (lddh < k || !aligned(dH, 2))) || (dW && (lddw < k || !aligned(dW, 2))))
+    return OS2_ERR_INVALID_ARG;
+  if (n > 0 && (!lse || !grad || !aligned(lse, 4) || !aligned(grad, 4))) return OS2_ERR_INVALID_ARG;
+  if (!dH && !dW) return OS2_OK;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (n == 0) {
+    if (!dW) return OS2_OK;
+    return cudaMemset2DAsync(dW, (size_t)lddw * 2, 0, (size_t)k * 2, (size_t)v, s) == cudaSuccess
+               ? OS2_OK
+               : OS2_ERR_CUDA;
+  }
+  const Layout L = layout(n, k, v, W, ldw, true);
+  if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256))
+    return OS2_ERR_WORKSPACE;
+  Prep p = {};
+  p.status = os2_status_ptr();
+  if (!p.status) return OS2_ERR_CUDA;
+  p.n = n;
+  p.k = k;
+  p.v = v;
+  p.H = static_cast<const uint16_t *>(H);
+  p.ldh = ldh;
+  p.labels = labels;
+  p.ignore = ignore_index;
+  p.lse_in = lse;
+  p.grad = grad;
+  p.f16 = dtype == OS2_F16;
+  p.dH = static_cast<uint16_t *>(dH);
+  p.lddh = lddh;
+  const uint16_t *w = static_cast<const uint16_t *>(W);
+  uint16_t *dw = static_cast<uint16_t *>(dW);
+  const cudaError_t e = dtype == OS2_BF16
+                            ? backward<true>(p, w, ldw, dw, lddw, workspace, L, s)
+                            : backward<false>(p, w, ldw, dw, lddw, workspace, L, s);
+  return e == cudaSuccess ? OS2_OK : OS2_ERR_CUDA;
+}

@@ -7,12 +7,13 @@
 // A few tokens (k_dot): the weights' bytes bound it.  A warp takes rows of B,
 // its lanes 16 bytes apart, four products an instruction (dp4a), every loaded
 // weight used for all tokens at once.
+// More tokens: k_i8tc.cu.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
 
-#include "os2_internal.cuh"
+#include "i8.cuh"
 
 namespace {
 
@@ -61,16 +62,48 @@ __device__ __forceinline__ int quant(float x, float s) {
 
 constexpr int kQThreads = 256;
 
+// 8 consecutive integers of which n are stored (vec: aligned for one store)
+__device__ __forceinline__ void store8(int8_t *dst, const int (&c)[8], int n, bool vec) {
+  if (vec && n >= 8) {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; i++) w[i >> 2] |= ((uint32_t)c[i] & 0xFFu) << (8 * (i & 3));
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      if (i < n) dst[i] = (int8_t)c[i];
+  }
+}
+__device__ __forceinline__ void store8(__half *dst, const int (&c)[8], int n, bool vec) {
+  if (vec && n >= 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const __half2 h = __floats2half2_rn((float)c[2 * i], (float)c[2 * i + 1]);
+      w[i] = reinterpret_cast<const uint32_t &>(h);
+    }
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      if (i < n) dst[i] = __float2half_rn((float)c[i]);
+  }
+}
+
 // One CTA a row: the row's largest magnitude, then its integers (the second
 // read comes from cache).  The maximum is taken of the bits of |x|, which order
-// as the values do and put Inf and NaN above every number.  Entries h in [k,
-// kz) are written as zeros.
-template <int DT>
+// as the values do and put Inf and NaN above every number.  Q: int8_t, or __half
+// for the tensor cores' tokens.  Entries h in [k, kz) are written as zeros, and
+// so are nzero counters of the kernel that follows.
+template <int DT, typename Q>
 __global__ void __launch_bounds__(kQThreads)
-    k_quant(int k, const void *X, long ldx, int8_t *q, long ldq, int kz, float *scale, bool vecx,
-            bool vecq) {
+    k_quant(int k, const void *X, long ldx, Q *q, long ldq, int kz, float *scale, bool vecx,
+            bool vecq, unsigned *zero, int nzero) {
   __shared__ uint32_t s_top[kQThreads / 32];
   const int row = blockIdx.x, tid = threadIdx.x;
+  if (row == 0)
+    for (int i = tid; i < nzero; i += kQThreads) zero[i] = 0;
   const char *x = static_cast<const char *>(X) + (size_t)row * ldx * (DT == OS2_F32 ? 4 : 2);
   uint32_t top = 0;
   for (int h = tid * 8; h < k; h += kQThreads * 8) {
@@ -87,23 +120,65 @@ __global__ void __launch_bounds__(kQThreads)
   const bool finite = top < 0x7F800000u;
   const float s = __fdiv_rn(__uint_as_float(top), 127.f);
   if (tid == 0) scale[row] = finite ? s : __uint_as_float(0x7FC00000u);
-  int8_t *dst = q + (size_t)row * ldq;
+  Q *dst = q + (size_t)row * ldq;
   for (int h = tid * 8; h < kz; h += kQThreads * 8) {
     float v[8];
     load8<DT>(x, h, k - h, vecx, v);
-    uint32_t w[2] = {0, 0};
+    int c[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      const int c = finite && s > 0.f ? quant(v[i], s) : 0;
-      w[i >> 2] |= ((uint32_t)c & 0xFFu) << (8 * (i & 3));
-    }
-    if (vecq && h + 8 <= kz) {
-      *reinterpret_cast<uint2 *>(dst + h) = make_uint2(w[0], w[1]);
+    for (int i = 0; i < 8; i++) c[i] = finite && s > 0.f ? quant(v[i], s) : 0;
+    store8(dst + h, c, kz - h, vecq);
+  }
+}
+
+// 8-bit tokens as FP16, one CTA a row.
+__global__ void __launch_bounds__(kQThreads)
+    k_widen_tokens(int k, const int8_t *A, long lda, __half *dst, long pitch, bool vec,
+                   unsigned *zero, int nzero) {
+  const int row = blockIdx.x, tid = threadIdx.x;
+  if (row == 0)
+    for (int i = tid; i < nzero; i += kQThreads) zero[i] = 0;
+  const int8_t *a = A + (size_t)row * lda;
+  for (int h = tid * 8; h < k; h += kQThreads * 8) {
+    int c[8];
+    if (vec && h + 8 <= k) {
+      const uint2 w = *reinterpret_cast<const uint2 *>(a + h);
+#pragma unroll
+      for (int i = 0; i < 8; i++) c[i] = (int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; i++)
-        if (h + i < kz) dst[h + i] = (int8_t)(w[i >> 2] >> (8 * (i & 3)));
+      for (int i = 0; i < 8; i++) c[i] = h + i < k ? a[h + i] : 0;
     }
+    store8(dst + (size_t)row * pitch + h, c, k - h, true);
+  }
+}
+
+// Rows of B off the 16-byte boundaries that TMA needs, copied onto them (only
+// for such B): 16 bytes a thread, read as words that straddle them.
+__global__ void __launch_bounds__(256)
+    k_align_rows(int n, int k, const int8_t *B, long ldb, int8_t *dst, long pitch) {
+  const long per = pitch / 16, total = per * n;
+  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
+    const long r = i / per;
+    const int h = (int)(i - r * per) * 16;
+    const int8_t *src = B + r * ldb + h;
+    uint32_t w[4];
+    if (h >= 4 && h + 20 <= k) {
+      const int o = (int)(reinterpret_cast<uintptr_t>(src) & 3);
+      const uint32_t *p = reinterpret_cast<const uint32_t *>(src - o);
+      uint32_t x[5];
+#pragma unroll
+      for (int q = 0; q < 5; q++) x[q] = __ldg(p + q);
+#pragma unroll
+      for (int q = 0; q < 4; q++) w[q] = __funnelshift_r(x[q], x[q + 1], 8 * o);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; q++) w[q] = 0;
+#pragma unroll
+      for (int q = 0; q < 16; q++)
+        if (h + q < k) w[q >> 2] |= (uint32_t)(uint8_t)src[q] << (8 * (q & 3));
+    }
+    *reinterpret_cast<uint4 *>(dst + r * pitch + h) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -236,54 +311,115 @@ bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 size_t elem_size(int dt) { return dt == OS2_F32 ? 4 : 2; }
 bool is_dtype(int dt) { return dt == OS2_F32 || dt == OS2_F16 || dt == OS2_BF16; }
 
+// Up to 8 tokens the weights are read once by k_dot; more go to the tensor cores.
 constexpr int kDotTokens = 8;
 
 cudaError_t dot(int ot, int m, int n, int k, const int8_t *T, long pitch, const float *sa,
                 const int8_t *B, long ldb, const float *sb, const float *bias, void *C, long ldc,
                 cudaStream_t s) {
   const bool al = aligned(B, 16) && ldb % 16 == 0;
-  for (int t0 = 0; t0 < m; t0 += kDotTokens) {
-    const int mt = std::min(kDotTokens, m - t0);
-    const int8_t *Tt = T + (size_t)t0 * pitch;
-    void *Ct = static_cast<char *>(C) + (size_t)t0 * ldc * elem_size(ot);
-#define DOT(M, R, U)                                                                              \
-  (al ? launch_dot_o<M, R, U, true>(ot, mt, n, k, Tt, pitch, sa + t0, B, ldb, sb, bias, Ct, ldc, s) \
-      : launch_dot_o<M, R, U, false>(ot, mt, n, k, Tt, pitch, sa + t0, B, ldb, sb, bias, Ct, ldc, s))
-    if (mt == 1) DOT(1, 1, 4);
-    else if (mt <= 4) DOT(4, 2, 2);
-    else DOT(8, 4, 1);
+#define DOT(M, R, U)                                                                          \
+  (al ? launch_dot_o<M, R, U, true>(ot, m, n, k, T, pitch, sa, B, ldb, sb, bias, C, ldc, s)   \
+      : launch_dot_o<M, R, U, false>(ot, m, n, k, T, pitch, sa, B, ldb, sb, bias, C, ldc, s))
+  if (m == 1) DOT(1, 1, 4);
+  else if (m <= 4) DOT(4, 2, 2);
+  else DOT(8, 4, 1);
 #undef DOT
-  }
   return cudaGetLastError();
 }
 
-struct Layout {
-  size_t tokens, scale, total;
-};
-Layout layout(int m, int k) {
-  Layout L;
-  L.tokens = 0;
-  L.scale = os2_round_up((size_t)m * token_pitch(k), 256);
-  L.total = L.scale + os2_round_up((size_t)m * 4, 256);
-  return L;
-}
-
-cudaError_t quantize(int m, int k, int dtype, const void *X, long ldx, int8_t *q, long ldq, int kz,
-                     float *scale, cudaStream_t s) {
+template <typename Q>
+cudaError_t quantize(int m, int k, int dtype, const void *X, long ldx, Q *q, long ldq, int kz,
+                     float *scale, cudaStream_t s, unsigned *zero = nullptr, int nzero = 0) {
   const bool vecx = aligned(X, 16) && (ldx * elem_size(dtype)) % 16 == 0;
-  const bool vecq = aligned(q, 8) && ldq % 8 == 0;
-  if (dtype == OS2_F32)
-    k_quant<OS2_F32><<<m, kQThreads, 0, s>>>(k, X, ldx, q, ldq, kz, scale, vecx, vecq);
-  else if (dtype == OS2_BF16)
-    k_quant<OS2_BF16><<<m, kQThreads, 0, s>>>(k, X, ldx, q, ldq, kz, scale, vecx, vecq);
-  else
-    k_quant<OS2_F16><<<m, kQThreads, 0, s>>>(k, X, ldx, q, ldq, kz, scale, vecx, vecq);
+  const bool vecq = aligned(q, 8 * sizeof(Q)) && ldq % 8 == 0;
+#define QUANT(DT) k_quant<DT, Q><<<m, kQThreads, 0, s>>>(k, X, ldx, q, ldq, kz, scale, vecx, vecq, zero, nzero)
+  if (dtype == OS2_F32) QUANT(OS2_F32);
+  else if (dtype == OS2_BF16) QUANT(OS2_BF16);
+  else QUANT(OS2_F16);
+#undef QUANT
   return cudaGetLastError();
 }
 
 // |sum| <= k 2^14 stays below 2^31
 constexpr int kMaxK = (1 << 17) - 1;
 constexpr int kMaxDim = 1 << 24;
+
+bool on_dot(int m, int k) { return m <= kDotTokens || k == 0; }
+
+struct Layout {
+  long pitch;                               // of the tokens
+  long wpitch;                              // of the copied weights, 0: as they lie
+  int counters;
+  size_t tokens, scale, done, slots, weights, total;
+};
+Layout layout(int m, int n, int k, const void *B, long ldb) {
+  Layout L = {};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += os2_round_up(bytes, 256);
+    return o;
+  };
+  const bool d = on_dot(m, k);
+  L.pitch = d ? token_pitch(k) : (long)os2_round_up((size_t)k, 8);
+  L.tokens = take((size_t)m * L.pitch * (d ? 1 : 2));
+  L.scale = take((size_t)m * 4);
+  if (!d && n > 0) {
+    const I8TcSizes z = i8tc_sizes(m, n, k);
+    L.counters = z.counters;
+    L.done = take((size_t)z.counters * 4);
+    L.slots = take(z.slot_ints * 4);
+    if (!aligned(B, 16) || ldb % 16) {
+      L.wpitch = (long)os2_round_up((size_t)k, 16);
+      L.weights = take((size_t)n * L.wpitch);
+    }
+  }
+  L.total = at;
+  return L;
+}
+
+// After the tokens are in the workspace.
+cudaError_t product(int m, int n, int k, const Layout &L, char *ws, const float *sa,
+                    const int8_t *B, long ldb, const float *sb, const float *bias, void *C,
+                    long ldc, int ot, int *status, cudaStream_t s) {
+  if (on_dot(m, k)) {
+    const int8_t *T = reinterpret_cast<const int8_t *>(ws + L.tokens);
+    for (int t = 0; t < m; t += kDotTokens) {  // more than one round with k = 0 only
+      const cudaError_t e = dot(ot, std::min(kDotTokens, m - t), n, k, T + t * L.pitch, L.pitch,
+                                sa + t, B, ldb, sb, bias,
+                                static_cast<char *>(C) + (size_t)t * ldc * elem_size(ot), ldc, s);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+  }
+  if (L.wpitch) {
+    int8_t *w = reinterpret_cast<int8_t *>(ws + L.weights);
+    const long pieces = L.wpitch / 16 * n;
+    k_align_rows<<<(unsigned)std::min<long>((pieces + 255) / 256, 16L * os2_sm_count()), 256, 0, s>>>(
+        n, k, B, ldb, w, L.wpitch);
+    B = w;
+    ldb = L.wpitch;
+  }
+  I8TcArgs a;
+  a.m = m;
+  a.n = n;
+  a.k = k;
+  a.tokens = ws + L.tokens;
+  a.pitch = L.pitch;
+  a.W = B;
+  a.ldw = ldb;
+  a.sa = sa;
+  a.sb = sb;
+  a.bias = bias;
+  a.y = C;
+  a.ldy = ldc;
+  a.out_dtype = ot;
+  a.slots = reinterpret_cast<int *>(ws + L.slots);
+  a.done = reinterpret_cast<unsigned *>(ws + L.done);
+  a.status = status;
+  return launch_i8tc(a, s);
+}
 
 os2_status check(int m, int n, int k, const void *A, int lda, const void *B, int ldb,
                  const float *sb, const float *bias, const void *C, int ldc, int ot) {
@@ -312,7 +448,7 @@ extern "C" os2_status os2_quantize_rows(int m, int k, int dtype, const void *X, 
 
 extern "C" size_t os2_i8gemm_workspace_size(int m, int n, int k, const void *B, int ldb) {
   if (m < 0 || n < 0 || k < 0 || k > kMaxK || m > kMaxDim || n > kMaxDim || ldb < k) return 0;
-  return layout(m, k).total;
+  return layout(m, n, k, B, ldb).total;
 }
 
 extern "C" os2_status os2_i8gemm(int m, int n, int k, const int8_t *A, int lda,
@@ -324,16 +460,22 @@ extern "C" os2_status os2_i8gemm(int m, int n, int k, const int8_t *A, int lda,
   if (st) return st;
   if (m == 0 || n == 0) return OS2_OK;
   if (!a_scale || !aligned(a_scale, 4)) return OS2_ERR_INVALID_ARG;
-  const Layout L = layout(m, k);
+  const Layout L = layout(m, n, k, B, ldb);
   if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256))
     return OS2_ERR_WORKSPACE;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int8_t *T = static_cast<int8_t *>(workspace) + L.tokens;
-  k_pack_tokens<<<m, 256, 0, s>>>(k, A, lda, T, token_pitch(k));
-  return dot(out_dtype, m, n, k, T, token_pitch(k), a_scale, B, ldb, b_scale, bias, C, ldc, s) ==
-                 cudaSuccess
-             ? OS2_OK
-             : OS2_ERR_CUDA;
+  int *status = os2_status_ptr();
+  if (!status) return OS2_ERR_CUDA;
+  char *ws = static_cast<char *>(workspace);
+  if (on_dot(m, k))
+    k_pack_tokens<<<m, 256, 0, s>>>(k, A, lda, reinterpret_cast<int8_t *>(ws + L.tokens), L.pitch);
+  else
+    k_widen_tokens<<<m, kQThreads, 0, s>>>(k, A, lda, reinterpret_cast<__half *>(ws + L.tokens),
+                                           L.pitch, aligned(A, 8) && lda % 8 == 0,
+                                           reinterpret_cast<unsigned *>(ws + L.done), L.counters);
+  const cudaError_t e = product(m, n, k, L, ws, a_scale, B, ldb, b_scale, bias, C, ldc, out_dtype,
+                                status, s);
+  return e == cudaSuccess ? OS2_OK : OS2_ERR_CUDA;
 }
 
 extern "C" os2_status os2_i8linear(int m, int n, int k, int dtype, const void *X, int ldx,
@@ -344,15 +486,21 @@ extern "C" os2_status os2_i8linear(int m, int n, int k, int dtype, const void *X
   const os2_status st = check(m, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, out_dtype);
   if (st) return st;
   if (m == 0 || n == 0) return OS2_OK;
-  const Layout L = layout(m, k);
+  const Layout L = layout(m, n, k, B, ldb);
   if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256))
     return OS2_ERR_WORKSPACE;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int8_t *T = static_cast<int8_t *>(workspace) + L.tokens;
-  float *sa = reinterpret_cast<float *>(static_cast<char *>(workspace) + L.scale);
-  const long pitch = token_pitch(k);
-  cudaError_t e = quantize(m, k, dtype, X, ldx, T + kPad, pitch, (int)(pitch - 2 * kPad), sa, s);
+  int *status = os2_status_ptr();
+  if (!status) return OS2_ERR_CUDA;
+  char *ws = static_cast<char *>(workspace);
+  float *sa = reinterpret_cast<float *>(ws + L.scale);
+  cudaError_t e =
+      on_dot(m, k)
+          ? quantize(m, k, dtype, X, ldx, reinterpret_cast<int8_t *>(ws + L.tokens) + kPad, L.pitch,
+                     (int)(L.pitch - 2 * kPad), sa, s)
+          : quantize(m, k, dtype, X, ldx, reinterpret_cast<__half *>(ws + L.tokens), L.pitch, k, sa,
+                     s, reinterpret_cast<unsigned *>(ws + L.done), L.counters);
   if (e == cudaSuccess)
-    e = dot(out_dtype, m, n, k, T, pitch, sa, B, ldb, b_scale, bias, C, ldc, s);
+    e = product(m, n, k, L, ws, sa, B, ldb, b_scale, bias, C, ldc, out_dtype, status, s);
   return e == cudaSuccess ? OS2_OK : OS2_ERR_CUDA;
 }

@@ -308,14 +308,14 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // A row-major matrix of 16-bit entries: `rows` rows of `cols` entries, `pitch`
 // entries apart.  mn: the terms run along the rows (box 64 x 64), else along
-// the columns (box 64 x 128).  base and pitch * 2 must be multiples of 16.
+// the columns (box 64 x box_rows).  base and pitch * 2 must be multiples of 16.
 inline bool make_map(CUtensorMap *map, const void *base, bool bf16, long cols, long rows,
-                     long pitch, bool mn) {
+                     long pitch, bool mn, int box_rows = kHalf) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
   cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)pitch * 2 * (cuuint64_t)rows};
-  cuuint32_t box[3] = {(cuuint32_t)kBK, (cuuint32_t)(mn ? kBK : kHalf), 1};
+  cuuint32_t box[3] = {(cuuint32_t)kBK, (cuuint32_t)(mn ? kBK : box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
             const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -269,6 +269,16 @@ __device__ __forceinline__ void umma2_f16(uint32_t d_tmem, uint64_t adesc, uint6
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// 2-SM MMA with A in tensor memory: each CTA's 128 lanes hold its 128 rows of A,
+// a 32-bit column two consecutive FP16 terms (8 columns for K = 16).
+__device__ __forceinline__ void umma2_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // Arrive on the mbarrier at this offset in every CTA of `mask` once all
 // prior 2-SM MMAs of this thread complete.
 __device__ __forceinline__ void umma2_commit_mc(uint64_t *bar, uint16_t mask) {

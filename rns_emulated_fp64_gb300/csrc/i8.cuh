@@ -1,8 +1,8 @@
-// The 8-bit product's tensor-core kernel (k_i8tc.cu), as its callers see it.
+// What the 8-bit product's kernels share (k_i8.cu, k_i8few.cu, k_i8tc.cu).
 #pragma once
-#include "os2_internal.cuh"
+#include "mm2.cuh"
 
-struct I8TcArgs {
+struct I8Args {
   int m, n, k;                 // tokens, channels, terms (k >= 1)
   const void *tokens;          // FP16 integers [m][pitch], pitch a multiple of 8, 16-byte aligned
   long pitch;
@@ -12,13 +12,181 @@ struct I8TcArgs {
   void *y;
   long ldy;
   int out_dtype;
-  int *slots;                  // I8TcSizes
+  bool overlap;                // W is the caller's: it may be read before the kernel in front ends
+  int *slots;                  // I8Sizes
   unsigned *done;              // zero before the launch
   int *status;
 };
-struct I8TcSizes {
+struct I8Sizes {
   int counters;                // of `done`
   size_t slot_ints;
 };
-I8TcSizes i8tc_sizes(int m, int n, int k);
-cudaError_t launch_i8tc(const I8TcArgs &a, cudaStream_t s);
+// k_i8few: m <= kI8Few tokens, mma.sync, no slots or counters; k_i8tc: tcgen05.
+constexpr int kI8Few = 32;
+cudaError_t launch_i8few(const I8Args &a, cudaStream_t s);
+I8Sizes i8tc_sizes(int m, int n, int k);
+cudaError_t launch_i8tc(const I8Args &a, cudaStream_t s);
+
+namespace os2i8 {
+
+using namespace os2mm;
+
+// The work: tiles of CH channels x NT tokens over stages of 128 terms.  Whole
+// tiles go round the workers; the last one or two per worker are cut along k as
+// well, so that all end together and few tiles still use all SMs.
+struct I8Job {
+  int m, n;            // tokens, channels
+  int tiles_c, tiles_t, stages;  // tiles of channels and tokens, stages of 128 terms
+  int waves;           // whole tiles of each worker (CTA, or pair of them)
+  int rest;            // tiles cut along k
+  int workers;
+  int few, more;       // units of a worker in the cut tiles: unit_begin
+  int out_dtype;
+  const float *sa, *sb, *bias;
+  void *y;
+  long ldy;
+  int *slots;          // [workers][2][2 CTAs][NT / 4][128][4] partial sums
+  unsigned *done;      // [rest][2] stages finished, zero before the launch
+};
+
+__device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  const uint32_t x = w ^ 0x80808080u;
+  lo = add2(__byte_perm(x, 0x64646464u, 0x4140), 0xE480E480u);  // - 1152
+  hi = add2(__byte_perm(x, 0x64646464u, 0x4342), 0xE480E480u);
+}
+
+// First unit (stage of a cut tile) of worker p: `few` + 1 units for the first
+// `more` workers, `few` for the others.
+__device__ __forceinline__ int unit_begin(const I8Job &j, int p) {
+  return p * j.few + min(p, j.more);
+}
+// The worker whose range holds unit u.
+__device__ __forceinline__ int worker_of(const I8Job &j, int u) {
+  const int big = j.more * (j.few + 1);
+  return u < big ? u / (j.few + 1) : j.more + (u - big) / j.few;
+}
+
+// The segments of a worker, in order: f(tile, first stage, end stage, index of the
+// cut tile or -1 for a whole one).  Every role walks the same.
+template <class F>
+__device__ __forceinline__ void for_segments(const I8Job &j, int worker, F &&f) {
+  const int u1 = unit_begin(j, worker + 1);
+  int w = 0;
+  for (int u = unit_begin(j, worker); w < j.waves || u < u1;) {
+    int t, s0 = 0, s1 = j.stages, cut = -1;
+    if (w < j.waves) {
+      t = w++ * j.workers + worker;
+    } else {
+      const int r = u / j.stages;
+      s0 = u - r * j.stages;
+      s1 = min(j.stages, s0 + u1 - u);
+      u += s1 - s0;
+      t = j.waves * j.workers + r;
+      if (s1 - s0 < j.stages) cut = r;
+    }
+    if (!f(t, s0, s1, cut)) return;
+  }
+}
+
+// The part of worker p in cut tile r is its first segment there (slot 0) unless
+// its range began in an earlier tile (slot 1).
+__device__ __forceinline__ int slot_of(const I8Job &j, int p, int r) {
+  return unit_begin(j, p) >= r * j.stages ? 0 : 1;
+}
+
+__device__ __forceinline__ void store_y(void *y, int dtype, size_t i, float v) {
+  if (dtype == OS2_F32) static_cast<float *>(y)[i] = v;
+  else if (dtype == OS2_BF16) static_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half *>(y)[i] = __float2half_rn(v);
+}
+
+// The other workers that hold parts of cut tile `r` are [first, last] less `me`.
+// Only the first may have begun in an earlier tile (slot 1).
+__device__ __forceinline__ void parts_of(const I8Job &j, int r, int &first, int &last) {
+  first = worker_of(j, r * j.stages);
+  last = worker_of(j, (r + 1) * j.stages - 1);
+}
+
+// How the eight warps of a CTA that hold a part of a cut tile learn whether it
+// was the last one: two barriers of shared memory (a: 8 arrivals, b: 1), waited
+// for with a limit like every other.
+struct I8Join {
+  uint64_t *a, *b;
+  volatile unsigned *last;
+  uint32_t parity;
+};
+// After the part (`mine` stages of a tile's `stages`) is in its slot; every lane
+// of the eight warps calls it, `elected` is true for one thread.  0: not the
+// last, 1: the last, -1: gave up.
+__device__ __forceinline__ int last_part(I8Join &jn, unsigned *counter, int mine, int stages,
+                                         bool elected, volatile int *s_abort) {
+  __threadfence();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(jn.a);
+  if (elected) {
+    if (!mbar_wait_bounded(jn.a, jn.parity, s_abort, kWaitLimit)) *s_abort = 1;
+    else {
+      const unsigned before = atomicAdd(counter, (unsigned)mine);
+      *jn.last = before + (unsigned)mine == (unsigned)stages;
+      __threadfence();
+      mbar_arrive(jn.b);
+    }
+  }
+  __syncwarp();
+  const bool ok = mbar_wait_bounded(jn.b, jn.parity, s_abort, kWaitLimit);
+  jn.parity ^= 1;
+  if (!__all_sync(0xffffffffu, ok)) return -1;
+  __threadfence();
+  return *jn.last ? 1 : 0;
+}
+
+template <int CH>
+I8Job i8_plan(int m, int n, int k, int nt, int workers) {
+  I8Job j = {};
+  j.m = m;
+  j.n = n;
+  j.tiles_c = (n + CH - 1) / CH;
+  j.tiles_t = (m + nt - 1) / nt;
+  j.stages = std::max((k + kStageK - 1) / kStageK, 1);
+  const long tiles = (long)j.tiles_c * j.tiles_t;
+  j.workers = (int)std::max<long>(1, std::min<long>(workers, tiles * j.stages));
+  // a remainder of tiles takes the last whole wave with it, so that a cut tile
+  // has few parts
+  j.waves = (int)(tiles / j.workers) - (tiles % j.workers && tiles >= j.workers ? 1 : 0);
+  j.rest = (int)(tiles - (long)j.waves * j.workers);
+  const int units = j.rest * j.stages;  // fewer than 2 workers * 1024
+  j.few = units / j.workers;
+  j.more = units % j.workers;
+  return j;
+}
+
+inline void i8_fill(I8Job &j, const I8Args &a) {
+  j.out_dtype = a.out_dtype;
+  j.sa = a.sa;
+  j.sb = a.sb;
+  j.bias = a.bias;
+  j.y = a.y;
+  j.ldy = a.ldy;
+  j.slots = a.slots;
+  j.done = a.done;
+}
+
+// 8-bit rows: box 128 terms x 128 rows, 128-byte swizzle.
+inline bool map_w(CUtensorMap *map, const void *base, long k, long rows, long pitch) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)k, (cuuint64_t)rows, 1};
+  cuuint64_t strides[2] = {(cuuint64_t)pitch, (cuuint64_t)pitch * (cuuint64_t)rows};
+  cuuint32_t box[3] = {(cuuint32_t)kStageK, (cuuint32_t)kHalf, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace os2i8

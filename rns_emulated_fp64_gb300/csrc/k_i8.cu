@@ -4,10 +4,8 @@
 // and the quantisation it needs:
 //   s_i = max_h |x_ih| / 127,  q_ih = clamp(rint(x_ih / s_i), -127, 127).
 //
-// A few tokens (k_dot): the weights' bytes bound it.  A warp takes rows of B,
-// its lanes 16 bytes apart, four products an instruction (dp4a), every loaded
-// weight used for all tokens at once.
-// More tokens: k_i8tc.cu.
+// Quantisation, layout and dispatch; the products are in k_i8few.cu (few tokens)
+// and k_i8tc.cu.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -94,14 +92,15 @@ __device__ __forceinline__ void store8(__half *dst, const int (&c)[8], int n, bo
 // One CTA a row: the row's largest magnitude, then its integers (the second
 // read comes from cache).  The maximum is taken of the bits of |x|, which order
 // as the values do and put Inf and NaN above every number.  Q: int8_t, or __half
-// for the tensor cores' tokens.  Entries h in [k, kz) are written as zeros, and
-// so are nzero counters of the kernel that follows.
+// for the products' tokens.  Also zeroes the nzero counters of the kernel that
+// follows, which may start before this one ends and waits for its end.
 template <int DT, typename Q>
 __global__ void __launch_bounds__(kQThreads)
-    k_quant(int k, const void *X, long ldx, Q *q, long ldq, int kz, float *scale, bool vecx,
+    k_quant(int k, const void *X, long ldx, Q *q, long ldq, float *scale, bool vecx,
             bool vecq, unsigned *zero, int nzero) {
   __shared__ uint32_t s_top[kQThreads / 32];
   const int row = blockIdx.x, tid = threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;");
   if (row == 0)
     for (int i = tid; i < nzero; i += kQThreads) zero[i] = 0;
   const char *x = static_cast<const char *>(X) + (size_t)row * ldx * (DT == OS2_F32 ? 4 : 2);
@@ -121,13 +120,13 @@ __global__ void __launch_bounds__(kQThreads)
   const float s = __fdiv_rn(__uint_as_float(top), 127.f);
   if (tid == 0) scale[row] = finite ? s : __uint_as_float(0x7FC00000u);
   Q *dst = q + (size_t)row * ldq;
-  for (int h = tid * 8; h < kz; h += kQThreads * 8) {
+  for (int h = tid * 8; h < k; h += kQThreads * 8) {
     float v[8];
     load8<DT>(x, h, k - h, vecx, v);
     int c[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) c[i] = finite && s > 0.f ? quant(v[i], s) : 0;
-    store8(dst + h, c, kz - h, vecq);
+    store8(dst + h, c, k - h, vecq);
   }
 }
 
@@ -135,6 +134,7 @@ __global__ void __launch_bounds__(kQThreads)
 __global__ void __launch_bounds__(kQThreads)
     k_widen_tokens(int k, const int8_t *A, long lda, __half *dst, long pitch, bool vec,
                    unsigned *zero, int nzero) {
+  asm volatile("griddepcontrol.launch_dependents;");
   const int row = blockIdx.x, tid = threadIdx.x;
   if (row == 0)
     for (int i = tid; i < nzero; i += kQThreads) zero[i] = 0;
@@ -182,158 +182,23 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// ------------------------------------------------------------- few tokens
-// Tokens in the workspace: 16 zero bytes, k integers, zeros to `pitch`.
-constexpr int kPad = 16;
-long token_pitch(int k) { return (long)os2_round_up((size_t)k, 16) + 2 * kPad; }
-
-__global__ void k_pack_tokens(int k, const int8_t *A, long lda, int8_t *dst, long pitch) {
-  const int8_t *a = A + (size_t)blockIdx.x * lda;
-  int8_t *d = dst + (size_t)blockIdx.x * pitch;
-  for (int h = threadIdx.x; h < pitch; h += blockDim.x)
-    d[h] = h >= kPad && h - kPad < k ? a[h - kPad] : 0;
-}
-
-template <int OT>
-__device__ __forceinline__ void store_y(void *y, size_t i, float v) {
-  if (OT == OS2_F32) static_cast<float *>(y)[i] = v;
-  else if (OT == OS2_BF16) static_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
-  else static_cast<__half *>(y)[i] = __float2half_rn(v);
-}
-
-// The 16 weights of a row at bytes [at, at + 16) of it, those outside [0, k) as 0.
-__device__ __forceinline__ uint4 load_w(const int8_t *row, int at, int k) {
-  if (at >= 0 && at + 16 <= k) return __ldg(reinterpret_cast<const uint4 *>(row + at));
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 16; i++)
-    if (at + i >= 0 && at + i < k) w[i >> 2] |= (uint32_t)(uint8_t)row[at + i] << (8 * (i & 3));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-// The 16 integers of a token that meet them (t: the token's h = 0).
-template <bool ALIGNED>
-__device__ __forceinline__ uint4 load_t(const int8_t *t, int at) {
-  if (ALIGNED) return __ldg(reinterpret_cast<const uint4 *>(t + at));
-  const uint32_t *w = reinterpret_cast<const uint32_t *>(t + (at & ~3));
-  const int sh = (at & 3) * 8;
-  uint32_t r[5];
-#pragma unroll
-  for (int i = 0; i < 5; i++) r[i] = __ldg(w + i);
-  return make_uint4(__funnelshift_r(r[0], r[1], sh), __funnelshift_r(r[1], r[2], sh),
-                    __funnelshift_r(r[2], r[3], sh), __funnelshift_r(r[3], r[4], sh));
-}
-
-constexpr int kDotThreads = 256;
-
-// M tokens at once (the last group of a call may have fewer), R rows of B a
-// warp, U loads of 16 bytes a lane and row in flight.  Rows of B that start off
-// a 16-byte boundary (ALIGNED false) are read in aligned pieces all the same,
-// and the tokens shifted against them.
-template <int M, int R, int U, bool ALIGNED, int OT>
-__global__ void __launch_bounds__(kDotThreads)
-    k_dot(int m, int n, int k, const int8_t *T, long pitch, const float *sa, const int8_t *B,
-          long ldb, const float *sb, const float *bias, void *C, long ldc) {
-  const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * (kDotThreads / 32);
-  const int groups = (n + R - 1) / R;
-  for (int g = blockIdx.x * (kDotThreads / 32) + (threadIdx.x >> 5); g < groups; g += warps) {
-    int acc[R][M];
-    const int8_t *row[R];
-    int off[R];
-#pragma unroll
-    for (int r = 0; r < R; r++) {
-      row[r] = B + (size_t)min(g * R + r, n - 1) * ldb;  // a row past the end: the last again
-      off[r] = ALIGNED ? 0 : (int)(reinterpret_cast<uintptr_t>(row[r]) & 15);
-#pragma unroll
-      for (int t = 0; t < M; t++) acc[r][t] = 0;
-    }
-    const int end = ALIGNED ? k : k + 15;  // pieces of 16 that meet [0, k) at any offset
-    for (int h = lane * 16; h < end; h += 512 * U) {
-      uint4 w[R][U];
-#pragma unroll
-      for (int u = 0; u < U; u++)
-#pragma unroll
-        for (int r = 0; r < R; r++)
-          w[r][u] = h + 512 * u < k + off[r] ? load_w(row[r], h + 512 * u - off[r], k)
-                                             : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int u = 0; u < U; u++) {
-        if (h + 512 * u >= end) break;
-#pragma unroll
-        for (int t = 0; t < M; t++) {
-          if (t >= m) break;
-          const int8_t *tok = T + (size_t)t * pitch + kPad;
-          uint4 x;
-          if (ALIGNED) x = load_t<true>(tok, h + 512 * u);
-#pragma unroll
-          for (int r = 0; r < R; r++) {
-            // a piece wholly past the row holds zeros; its tokens are not read
-            if (!ALIGNED) x = load_t<false>(tok, min(h + 512 * u - off[r], k - 1));
-            int a = acc[r][t];
-            a = __dp4a((int)w[r][u].x, (int)x.x, a);
-            a = __dp4a((int)w[r][u].y, (int)x.y, a);
-            a = __dp4a((int)w[r][u].z, (int)x.z, a);
-            a = __dp4a((int)w[r][u].w, (int)x.w, a);
-            acc[r][t] = a;
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < R; r++)
-#pragma unroll
-      for (int t = 0; t < M; t++) {
-        const int sum = __reduce_add_sync(0xffffffffu, acc[r][t]);
-        const int j = g * R + r;
-        if (lane == r * M + t && t < m && j < n) {
-          const float y = (float)sum * sa[t] * sb[j];
-          store_y<OT>(C, (size_t)t * ldc + j, bias ? y + bias[j] : y);
-        }
-      }
-  }
-}
-
-template <int M, int R, int U, bool ALIGNED>
-void launch_dot_o(int ot, int m, int n, int k, const int8_t *T, long pitch, const float *sa,
-                  const int8_t *B, long ldb, const float *sb, const float *bias, void *C, long ldc,
-                  cudaStream_t s) {
-  const int groups = (n + R - 1) / R, per = kDotThreads / 32;
-  const int grid = std::min((groups + per - 1) / per, 8 * os2_sm_count());
-  if (ot == OS2_F32)
-    k_dot<M, R, U, ALIGNED, OS2_F32><<<grid, kDotThreads, 0, s>>>(m, n, k, T, pitch, sa, B, ldb, sb, bias, C, ldc);
-  else if (ot == OS2_BF16)
-    k_dot<M, R, U, ALIGNED, OS2_BF16><<<grid, kDotThreads, 0, s>>>(m, n, k, T, pitch, sa, B, ldb, sb, bias, C, ldc);
-  else
-    k_dot<M, R, U, ALIGNED, OS2_F16><<<grid, kDotThreads, 0, s>>>(m, n, k, T, pitch, sa, B, ldb, sb, bias, C, ldc);
+// Without terms, the bias.
+__global__ void k_bias(int m, int n, const float *bias, void *y, long ldy, int dtype) {
+  const long total = (long)m * n;
+  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256)
+    os2i8::store_y(y, dtype, (size_t)(i / n) * ldy + i % n, bias ? bias[i % n] : 0.f);
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 size_t elem_size(int dt) { return dt == OS2_F32 ? 4 : 2; }
 bool is_dtype(int dt) { return dt == OS2_F32 || dt == OS2_F16 || dt == OS2_BF16; }
 
-// Up to 8 tokens the weights are read once by k_dot; more go to the tensor cores.
-constexpr int kDotTokens = 8;
-
-cudaError_t dot(int ot, int m, int n, int k, const int8_t *T, long pitch, const float *sa,
-                const int8_t *B, long ldb, const float *sb, const float *bias, void *C, long ldc,
-                cudaStream_t s) {
-  const bool al = aligned(B, 16) && ldb % 16 == 0;
-#define DOT(M, R, U)                                                                          \
-  (al ? launch_dot_o<M, R, U, true>(ot, m, n, k, T, pitch, sa, B, ldb, sb, bias, C, ldc, s)   \
-      : launch_dot_o<M, R, U, false>(ot, m, n, k, T, pitch, sa, B, ldb, sb, bias, C, ldc, s))
-  if (m == 1) DOT(1, 1, 4);
-  else if (m <= 4) DOT(4, 2, 2);
-  else DOT(8, 4, 1);
-#undef DOT
-  return cudaGetLastError();
-}
-
 template <typename Q>
-cudaError_t quantize(int m, int k, int dtype, const void *X, long ldx, Q *q, long ldq, int kz,
+cudaError_t quantize(int m, int k, int dtype, const void *X, long ldx, Q *q, long ldq,
                      float *scale, cudaStream_t s, unsigned *zero = nullptr, int nzero = 0) {
   const bool vecx = aligned(X, 16) && (ldx * elem_size(dtype)) % 16 == 0;
   const bool vecq = aligned(q, 8 * sizeof(Q)) && ldq % 8 == 0;
-#define QUANT(DT) k_quant<DT, Q><<<m, kQThreads, 0, s>>>(k, X, ldx, q, ldq, kz, scale, vecx, vecq, zero, nzero)
+#define QUANT(DT) k_quant<DT, Q><<<m, kQThreads, 0, s>>>(k, X, ldx, q, ldq, scale, vecx, vecq, zero, nzero)
   if (dtype == OS2_F32) QUANT(OS2_F32);
   else if (dtype == OS2_BF16) QUANT(OS2_BF16);
   else QUANT(OS2_F16);
@@ -345,7 +210,9 @@ cudaError_t quantize(int m, int k, int dtype, const void *X, long ldx, Q *q, lon
 constexpr int kMaxK = (1 << 17) - 1;
 constexpr int kMaxDim = 1 << 24;
 
-bool on_dot(int m, int k) { return m <= kDotTokens || k == 0; }
+// Up to 32 tokens the stream of weights is the bound and mma.sync keeps up with
+// it; more go to tcgen05.
+bool few(int m) { return m <= kI8Few; }
 
 struct Layout {
   long pitch;                               // of the tokens
@@ -361,15 +228,16 @@ Layout layout(int m, int n, int k, const void *B, long ldb) {
     at += os2_round_up(bytes, 256);
     return o;
   };
-  const bool d = on_dot(m, k);
-  L.pitch = d ? token_pitch(k) : (long)os2_round_up((size_t)k, 8);
-  L.tokens = take((size_t)m * L.pitch * (d ? 1 : 2));
+  L.pitch = (long)os2_round_up((size_t)k, 8);
+  L.tokens = take((size_t)m * L.pitch * 2);
   L.scale = take((size_t)m * 4);
-  if (!d && n > 0) {
-    const I8TcSizes z = i8tc_sizes(m, n, k);
-    L.counters = z.counters;
-    L.done = take((size_t)z.counters * 4);
-    L.slots = take(z.slot_ints * 4);
+  if (k > 0 && n > 0 && m > 0) {
+    if (!few(m)) {
+      const I8Sizes z = i8tc_sizes(m, n, k);
+      L.counters = z.counters;
+      L.done = take((size_t)z.counters * 4);
+      L.slots = take(z.slot_ints * 4);
+    }
     if (!aligned(B, 16) || ldb % 16) {
       L.wpitch = (long)os2_round_up((size_t)k, 16);
       L.weights = take((size_t)n * L.wpitch);
@@ -379,20 +247,11 @@ Layout layout(int m, int n, int k, const void *B, long ldb) {
   return L;
 }
 
-// After the tokens are in the workspace.
+// After the tokens are in the workspace (k >= 1).
 cudaError_t product(int m, int n, int k, const Layout &L, char *ws, const float *sa,
                     const int8_t *B, long ldb, const float *sb, const float *bias, void *C,
                     long ldc, int ot, int *status, cudaStream_t s) {
-  if (on_dot(m, k)) {
-    const int8_t *T = reinterpret_cast<const int8_t *>(ws + L.tokens);
-    for (int t = 0; t < m; t += kDotTokens) {  // more than one round with k = 0 only
-      const cudaError_t e = dot(ot, std::min(kDotTokens, m - t), n, k, T + t * L.pitch, L.pitch,
-                                sa + t, B, ldb, sb, bias,
-                                static_cast<char *>(C) + (size_t)t * ldc * elem_size(ot), ldc, s);
-      if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
-  }
+  const bool overlap = !L.wpitch;
   if (L.wpitch) {
     int8_t *w = reinterpret_cast<int8_t *>(ws + L.weights);
     const long pieces = L.wpitch / 16 * n;
@@ -401,7 +260,7 @@ cudaError_t product(int m, int n, int k, const Layout &L, char *ws, const float 
     B = w;
     ldb = L.wpitch;
   }
-  I8TcArgs a;
+  I8Args a;
   a.m = m;
   a.n = n;
   a.k = k;
@@ -418,7 +277,8 @@ cudaError_t product(int m, int n, int k, const Layout &L, char *ws, const float 
   a.slots = reinterpret_cast<int *>(ws + L.slots);
   a.done = reinterpret_cast<unsigned *>(ws + L.done);
   a.status = status;
-  return launch_i8tc(a, s);
+  a.overlap = overlap;
+  return few(m) ? launch_i8few(a, s) : launch_i8tc(a, s);
 }
 
 os2_status check(int m, int n, int k, const void *A, int lda, const void *B, int ldb,
@@ -440,7 +300,7 @@ extern "C" os2_status os2_quantize_rows(int m, int k, int dtype, const void *X, 
   if (m == 0) return OS2_OK;
   if (!scale || !aligned(scale, 4) || (k > 0 && (!X || !q || !aligned(X, elem_size(dtype)))))
     return OS2_ERR_INVALID_ARG;
-  return quantize(m, k, dtype, X, ldx, q, ldq, k, scale, static_cast<cudaStream_t>(stream)) ==
+  return quantize(m, k, dtype, X, ldx, q, ldq, scale, static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? OS2_OK
              : OS2_ERR_CUDA;
@@ -466,13 +326,15 @@ extern "C" os2_status os2_i8gemm(int m, int n, int k, const int8_t *A, int lda,
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   int *status = os2_status_ptr();
   if (!status) return OS2_ERR_CUDA;
+  if (k == 0) {
+    k_bias<<<std::min<long>(((long)m * n + 255) / 256, 8L * os2_sm_count()), 256, 0, s>>>(
+        m, n, bias, C, ldc, out_dtype);
+    return cudaGetLastError() == cudaSuccess ? OS2_OK : OS2_ERR_CUDA;
+  }
   char *ws = static_cast<char *>(workspace);
-  if (on_dot(m, k))
-    k_pack_tokens<<<m, 256, 0, s>>>(k, A, lda, reinterpret_cast<int8_t *>(ws + L.tokens), L.pitch);
-  else
-    k_widen_tokens<<<m, kQThreads, 0, s>>>(k, A, lda, reinterpret_cast<__half *>(ws + L.tokens),
-                                           L.pitch, aligned(A, 8) && lda % 8 == 0,
-                                           reinterpret_cast<unsigned *>(ws + L.done), L.counters);
+  k_widen_tokens<<<m, kQThreads, 0, s>>>(k, A, lda, reinterpret_cast<__half *>(ws + L.tokens),
+                                         L.pitch, aligned(A, 8) && lda % 8 == 0,
+                                         reinterpret_cast<unsigned *>(ws + L.done), L.counters);
   const cudaError_t e = product(m, n, k, L, ws, a_scale, B, ldb, b_scale, bias, C, ldc, out_dtype,
                                 status, s);
   return e == cudaSuccess ? OS2_OK : OS2_ERR_CUDA;
@@ -492,14 +354,15 @@ extern "C" os2_status os2_i8linear(int m, int n, int k, int dtype, const void *X
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   int *status = os2_status_ptr();
   if (!status) return OS2_ERR_CUDA;
+  if (k == 0) {
+    k_bias<<<std::min<long>(((long)m * n + 255) / 256, 8L * os2_sm_count()), 256, 0, s>>>(
+        m, n, bias, C, ldc, out_dtype);
+    return cudaGetLastError() == cudaSuccess ? OS2_OK : OS2_ERR_CUDA;
+  }
   char *ws = static_cast<char *>(workspace);
   float *sa = reinterpret_cast<float *>(ws + L.scale);
-  cudaError_t e =
-      on_dot(m, k)
-          ? quantize(m, k, dtype, X, ldx, reinterpret_cast<int8_t *>(ws + L.tokens) + kPad, L.pitch,
-                     (int)(L.pitch - 2 * kPad), sa, s)
-          : quantize(m, k, dtype, X, ldx, reinterpret_cast<__half *>(ws + L.tokens), L.pitch, k, sa,
-                     s, reinterpret_cast<unsigned *>(ws + L.done), L.counters);
+  cudaError_t e = quantize(m, k, dtype, X, ldx, reinterpret_cast<__half *>(ws + L.tokens), L.pitch,
+                           sa, s, reinterpret_cast<unsigned *>(ws + L.done), L.counters);
   if (e == cudaSuccess)
     e = product(m, n, k, L, ws, sa, B, ldb, b_scale, bias, C, ldc, out_dtype, status, s);
   return e == cudaSuccess ? OS2_OK : OS2_ERR_CUDA;

@@ -1,0 +1,370 @@
+// The 8-bit product of k_i8.cu for few tokens, where the weights' bytes bound it.
+//
+// A CTA streams its share of the weights through a ring of TMA copies (up to 200
+// KB an SM in flight, whatever the registers hold) with the tokens' matching
+// terms beside them.  Eight warps take 16 channels each of a stage of 128
+// channels x 128 terms: a lane reads 16 bytes of two channels at a time, widens
+// them to FP16 in registers (exact) and multiplies with mma.sync.m16n8k16, whose
+// fragments are the lanes' own bytes: the 16 terms of an instruction may be any,
+// as long as the tokens' are the same, so lane t's 16 consecutive bytes serve four
+// instructions.  tcgen05 would need the FP16 weights back in shared memory
+// (k_i8tc.cu: half the rate for 16 tokens).  FP32 accumulators are exact for 1024
+// terms (2^24); they are emptied into int32 after those.
+//
+// A cluster of C CTAs takes a tile of 128 channels, each CTA its C-th of the terms,
+// so that a few thousand channels already use every SM.  The int32 sums of a
+// channel meet in the CTA that stores it, sent there through distributed shared
+// memory by stores whose bytes the receiving warp waits for.  (Parts joined
+// through global memory, with stages dealt out evenly over single CTAs, took 3 us
+// longer: 12.5 us instead of 8 for 4096 x 4096 and one token.)
+//
+// Warps (9): 0-7 as above, 8 TMA.  The first weights are asked for before the kernel waits
+// for the one in front of it on the stream, which quantises the tokens: they are
+// inputs of the call, and nothing in front of that kernel can be writing them
+// still.  Every wait is bounded, as in mm2.cuh.
+#include <limits.h>
+
+#include "i8.cuh"
+
+using namespace os2i8;
+
+namespace {
+
+constexpr int kFewWarps = 8, kFewThreads = 32 * kFewWarps + 32;
+constexpr uint32_t kFewW = 128 * kStageK;        // a stage's weights
+
+template <int NG>
+struct Few {
+  static constexpr uint32_t block = NG * 8 * kBK * 2;        // one k-block of the tokens
+  static constexpr uint32_t stage = kFewW + 2 * block;
+  static constexpr uint32_t part = kFewWarps * NG * 32 * 16;  // a tile's sums, one side
+  static constexpr int stages = (int)((227 * 1024 - 1024 - 512 - 2 * part) / stage);
+  static constexpr size_t smem = 1024 + (size_t)stages * stage + 2 * part + 512;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
+struct FewJob {
+  int m, n, tiles, stages;
+  int cluster, clusters;     // CTAs of a cluster (1, 2, 4 or 8), clusters of the grid
+  int out_dtype;
+  const float *sa, *sb, *bias;
+  void *y;
+  long ldy;
+};
+
+template <int NG>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    k_i8few(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapT,
+            const FewJob j, int *status) {
+  using F = Few<NG>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+  uint8_t *sPart = smem + F::stages * F::stage;
+  uint64_t *full = reinterpret_cast<uint64_t *>(sPart + 2 * F::part);
+  uint64_t *empty = full + F::stages, *part = empty + F::stages;  // part: [2][kFewWarps]
+  volatile int *s_abort = reinterpret_cast<volatile int *>(part + 2 * kFewWarps);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank(), first = (int)blockIdx.x / j.cluster;
+  // this CTA's stages of every tile
+  const int s0 = rank * j.stages / j.cluster, s1 = (rank + 1) * j.stages / j.cluster;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < F::stages; s++) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kFewWarps);
+    }
+    for (int s = 0; s < 2 * kFewWarps; s++) mbar_init(&part[s], 1);
+    *s_abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&mapW);
+    tma_prefetch_desc(&mapT);
+  }
+  __syncthreads();
+  cluster_arrive();  // waited for before anything is sent to another CTA
+
+  auto gave_up = [&]() {
+    *s_abort = 1;
+    set_status(status, OS2_ERR_TIMEOUT);
+    return false;
+  };
+
+  if (warp == kFewWarps) {
+    // ------------------------------------------------------------ TMA
+    if (lane == 0) {
+      auto weights = [&](int st, int tc, int ks) {
+        mbar_arrive_expect_tx(&full[st], F::stage);
+        tma_load_3d(smem + st * F::stage, &mapW, &full[st], ks * kStageK, tc * 128, 0);
+      };
+      auto tokens = [&](int st, int ks) {
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+          tma_load_3d(smem + st * F::stage + kFewW + h * F::block, &mapT, &full[st],
+                      ks * kStageK + h * kBK, 0, 0);
+      };
+      // the first turn of the ring: weights, then, once they are there, tokens
+      int i = 0;
+      for (int t = first; t < j.tiles && i < F::stages; t += j.clusters)
+        for (int ks = s0; ks < s1 && i < F::stages; ks++) weights(i++, t, ks);
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      int st = 0;
+      uint32_t ph = 0, used = 0, last_par = 0;
+      bool ok = true;
+      i = 0;
+      for (int t = first; ok && t < j.tiles; t += j.clusters)
+        for (int ks = s0; ks < s1; ks++, i++) {
+          if (i >= F::stages) {
+            if (!mbar_wait_bounded(&empty[st], ph ^ 1, s_abort, kWaitLimit)) {
+              ok = gave_up();
+              break;
+            }
+            weights(st, t, ks);
+          }
+          tokens(st, ks);
+          used |= 1u << st;
+          last_par = (last_par & ~(1u << st)) | (ph << st);
+          if (++st == F::stages) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      for (int s = 0; s < F::stages; s++)
+        if (used >> s & 1) {
+          volatile int no_abort = 0;
+          mbar_wait_bounded(&full[s], (last_par >> s) & 1, &no_abort, kWaitLimit);
+        }
+    }
+    __syncwarp();
+    cluster_wait();
+  } else {
+    // ------------------------------------------------------------ products
+    const int g = lane >> 2, t4 = lane & 3;
+    // 16-byte piece c of a 128-byte row r of a swizzled block: c ^ (r & 7), and r & 7 == g
+    const uint32_t w0 = (uint32_t)(warp * 16 + g) * 128, w1 = w0 + 8 * 128;
+    int st = 0;
+    uint32_t ph = 0;
+    // Entry (q, e) of a thread: channel ch + 8 (e / 2), token 8 q + 2 t4 + e % 2.  The
+    // channels of lane row g meet in CTA g C / 8 of the cluster.  A warp sends the
+    // sums of tile i + 2 after it has had everyone's of tile i + 1, which their warps
+    // sent after they had read tile i: two sides are enough.
+    const int owner = g * j.cluster / 8;
+    const bool mine = owner == rank;
+    bool waited = false;  // for the kernel in front, and for the cluster
+    bool ok = true;
+    int side = 0;
+    uint32_t pph = 0;
+    for (int t = first; ok && t < j.tiles; t += j.clusters) {
+      float acc[NG][4];
+      int sum[NG][4];
+#pragma unroll
+      for (int q = 0; q < NG; q++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc[q][e] = 0.f, sum[q][e] = 0;
+      const int ch = t * 128 + warp * 16 + g;
+      float sb[2], bias[2];
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const bool in = ch + 8 * h < j.n;
+        sb[h] = in ? j.sb[ch + 8 * h] : 0.f;
+        bias[h] = in && j.bias ? j.bias[ch + 8 * h] : 0.f;
+      }
+      for (int ks = s0; ks < s1; ks++) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[st], ph, s_abort, kWaitLimit));
+        if (!ok) break;
+        const uint32_t base = smem_u32(smem + st * F::stage);
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const uint32_t at = (uint32_t)((4 * h + t4) ^ g) << 4;
+          const uint4 a = lds16(base + w0 + at), b = lds16(base + w1 + at);
+          uint4 x[NG][2];
+#pragma unroll
+          for (int q = 0; q < NG; q++)
+#pragma unroll
+            for (int e = 0; e < 2; e++)  // the same 16 terms of token q * 8 + g
+              x[q][e] = lds16(base + kFewW + h * F::block + (uint32_t)(q * 8 + g) * 128 +
+                              ((uint32_t)((2 * t4 + e) ^ g) << 4));
+          const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            uint32_t a0, a1, a2, a3;
+            widen(wa[e], a0, a2);
+            widen(wb[e], a1, a3);
+#pragma unroll
+            for (int q = 0; q < NG; q++) {
+              const uint4 xx = x[q][e >> 1];
+              mma16816(acc[q], a0, a1, a2, a3, e & 1 ? xx.z : xx.x, e & 1 ? xx.w : xx.y);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+        if (++st == F::stages) {
+          st = 0;
+          ph ^= 1;
+        }
+        if ((ks - s0) % 8 == 7 || ks == s1 - 1) {
+#pragma unroll
+          for (int q = 0; q < NG; q++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) sum[q][e] += __float2int_rn(acc[q][e]), acc[q][e] = 0.f;
+        }
+      }
+      if (!ok) break;
+      if (!waited) {  // the tokens' scales and the output; the other CTAs' barriers
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        cluster_wait();
+        waited = true;
+      }
+      if (j.cluster > 1) {
+        // the parts of a channel's C CTAs lie side by side: [C][8 / C lane rows] lanes
+        const uint32_t bar = smem_u32(&part[side * kFewWarps + warp]);
+        const uint32_t buf = smem_u32(sPart + side * F::part);
+        const int per = 32 / j.cluster;  // lanes of a part
+        const uint32_t to = mapa_shared(buf, owner) + (uint32_t)warp * NG * 512 +
+                            (uint32_t)(rank * per + (lane & (per - 1))) * 16;
+        const uint32_t to_bar = mapa_shared(bar, owner);
+        if (lane == 0) mbar_arrive_expect_tx(&part[side * kFewWarps + warp], NG * 512);
+#pragma unroll
+        for (int q = 0; q < NG; q++)
+          st_async16(to + q * 512, to_bar, sum[q][0], sum[q][1], sum[q][2], sum[q][3]);
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&part[side * kFewWarps + warp], pph, s_abort,
+                                                       kWaitLimit));
+        if (!ok) break;
+        const uint32_t from = buf + (uint32_t)warp * NG * 512 + (uint32_t)(lane & (per - 1)) * 16;
+#pragma unroll
+        for (int q = 0; q < NG; q++) {
+          int4 v = make_int4(0, 0, 0, 0);
+          for (int p = 0; p < j.cluster; p++) {
+            const uint4 x = lds16(from + q * 512 + (uint32_t)(p * per) * 16);
+            v.x += (int)x.x;
+            v.y += (int)x.y;
+            v.z += (int)x.z;
+            v.w += (int)x.w;
+          }
+          sum[q][0] = v.x;
+          sum[q][1] = v.y;
+          sum[q][2] = v.z;
+          sum[q][3] = v.w;
+        }
+        side ^= 1;
+        if (side == 0) pph ^= 1;
+      }
+      if (mine)
+#pragma unroll
+        for (int q = 0; q < NG; q++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const int c = ch + 8 * (e >> 1), to = q * 8 + 2 * t4 + (e & 1);
+            if (c < j.n && to < j.m)
+              store_y(j.y, j.out_dtype, (size_t)to * j.ldy + c,
+                      (float)sum[q][e] * j.sa[to] * sb[e >> 1] + bias[e >> 1]);
+          }
+      __syncwarp();
+    }
+    if (!ok) gave_up();
+    if (!waited) cluster_wait();
+  }
+  // no CTA leaves while another may still send to it
+  __syncwarp();
+  cluster_sync();
+}
+
+// Clusters of c CTAs that run at once on the device.
+template <int NG>
+int clusters_of(int c) {
+  static std::mutex mu;
+  static int known[9] = {};
+  std::lock_guard<std::mutex> g(mu);
+  if (!known[c]) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {(unsigned)c, 1, 1};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(os2_sm_count() / c * c));
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = Few<NG>::smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int v = 0;
+    if (cudaOccupancyMaxActiveClusters(&v, k_i8few<NG>, &cfg) != cudaSuccess) v = 0;
+    known[c] = std::max(1, std::min(v, os2_sm_count() / c));
+  }
+  return known[c];
+}
+
+template <int NG>
+cudaError_t launch(const I8Args &a, cudaStream_t s) {
+  using F = Few<NG>;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(k_i8few<NG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)F::smem);
+  });
+  if (attr_err != cudaSuccess) return attr_err;
+  FewJob j;
+  j.m = a.m;
+  j.n = a.n;
+  j.tiles = (a.n + 127) / 128;
+  j.stages = (a.k + kStageK - 1) / kStageK;
+  // the cluster size whose busiest CTA has the fewest stages; a larger one has to
+  // save more than one
+  long least = LONG_MAX;
+  for (const int c : {1, 2, 4, 8}) {
+    if (c > j.stages) break;
+    const int n = std::min(clusters_of<NG>(c), j.tiles);
+    const long t = (long)((j.tiles + n - 1) / n) * ((j.stages + c - 1) / c) + 1;
+    if (t < least) {
+      least = t - 1;
+      j.cluster = c;
+      j.clusters = n;
+    }
+  }
+  CUtensorMap mw, mt;
+  if (!map_w(&mw, a.W, a.k, a.n, a.ldw) ||
+      !make_map(&mt, a.tokens, false, a.k, a.m, a.pitch, false, NG * 8))
+    return cudaErrorInvalidValue;
+  j.out_dtype = a.out_dtype;
+  j.sa = a.sa;
+  j.sb = a.sb;
+  j.bias = a.bias;
+  j.y = a.y;
+  j.ldy = a.ldy;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)j.cluster, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(j.cluster * j.clusters));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = F::smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.overlap ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_i8few<NG>, mw, mt, j, a.status);
+}
+
+int groups(int m) { return m <= 8 ? 1 : m <= 16 ? 2 : 4; }
+
+}  // namespace
+
+cudaError_t launch_i8few(const I8Args &a, cudaStream_t s) {
+  const int g = groups(a.m);
+  return g == 1 ? launch<1>(a, s) : g == 2 ? launch<2>(a, s) : launch<4>(a, s);
+}

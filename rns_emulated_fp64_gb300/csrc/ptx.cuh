@@ -73,6 +73,18 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// Moves registers between the warpgroups of a block (all warps of a warpgroup
+// execute it; the sum over the warpgroups must not pass what the block was
+// launched with).
+template <int N>
+__device__ __forceinline__ void regs_fewer() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ----------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -213,6 +225,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
+// The same where no generic-proxy memory is handed over, only tensor memory
+// (ordered by tcgen05.wait and the tcgen05 fences) or the right to reuse a
+// buffer: without the release at cluster scope, whose fence costs the arriving
+// thread the better part of a microsecond.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -234,6 +253,21 @@ __device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t *bar, uint32_
     if (*abort) return false;
     if (clock64() - t0 > limit) return false;
   }
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+// 16 bytes to shared memory of a CTA of the cluster; their arrival counts as
+// bytes on an mbarrier of that CTA (both shared::cluster addresses).
+__device__ __forceinline__ void st_async16(uint32_t addr, uint32_t bar, int a, int b, int c, int d) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.s32 [%0], {%2,%3,%4,%5}, [%1];" ::"r"(
+          addr),
+      "r"(bar), "r"(a), "r"(b), "r"(c), "r"(d)
+      : "memory");
 }
 // TMA load into this CTA's shared memory whose completion is signalled on an
 // mbarrier in either CTA of the pair (shared::cluster address).

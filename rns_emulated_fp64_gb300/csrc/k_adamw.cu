@@ -12,9 +12,13 @@
 // never becomes 0 (code 1 at least): the update it divides stays bounded.
 //
 // Bound by memory: every byte is read or written once, 28 bytes an element
-// with FP32 parameters, gradients and moments.  A warp takes 256 elements (one
-// 8-bit block), a lane 8 consecutive ones, all loads before the arithmetic:
-// 8 (2 e_p + e_g + ...) bytes a lane are in flight, more than 100 KB an SM.
+// with FP32 parameters, gradients and moments.  A warp takes 256 elements (an 8-bit
+// block), a lane 8 consecutive ones, all loads before the arithmetic: more than 100
+// KB an SM in flight with FP32 moments.  With 8-bit ones the bytes are fewer and
+// the arithmetic (some 50 instructions an element) weighs as much as they do: six
+// CTAs an SM rather than five are worth 6 %, conversions are additions of 2^23 and
+// 1.5 2^23 instead of I2F and F2I, which run at a quarter of the rate, and the
+// exact rounding is taken only where the fast one is in doubt.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -27,7 +31,8 @@ namespace {
 
 constexpr int kBlock = 256;           // elements of a warp, and of an 8-bit scale
 constexpr int kThreads = 256;
-constexpr int kChunk = kBlock * kThreads / 32;
+constexpr int kWarps = kThreads / 32;
+constexpr int kChunk = kBlock * kWarps;  // of a CTA
 constexpr int kMaxTensors = 256;      // of one launch: 20 KB of kernel parameters
 
 struct Tensors {
@@ -111,35 +116,99 @@ __device__ __forceinline__ void store8(T *dst, const T (&x)[8], int n, bool vec)
   }
 }
 
-// The values of codes; the products are rounded one by one, so that every
-// reader of a state sees the same FP32 value.
-__device__ __forceinline__ float m_value(int c, float a) {
-  const float t = __fmul_rn((float)c, 1.0f / 127.0f);
+// The values of codes c (as FP32); the products are rounded one by one, so that
+// every reader of a state sees the same FP32 value.
+__device__ __forceinline__ float m_value(float c, float a) {
+  const float t = __fmul_rn(c, 1.0f / 127.0f);
   return __fmul_rn(a, __fmul_rn(t, fabsf(t)));
 }
-__device__ __forceinline__ float v_value(int c, float a) {
-  float t = __fmul_rn((float)c, 1.0f / 255.0f);
+__device__ __forceinline__ float v_value(float c, float a) {
+  float t = __fmul_rn(c, 1.0f / 255.0f);
   t = __fmul_rn(t, t);
   return __fmul_rn(a, __fmul_rn(t, t));
 }
-// The nearest code of m / a, of v / a (a > 0).
-__device__ __forceinline__ int m_code(float m, float a) {
-  const float q = rintf(__fmul_rn(__fsqrt_rn(__fdiv_rn(fabsf(m), a)), 127.0f));
-  return (int)copysignf(q, m);
+// Codes of eight moments from their bytes in two words.
+__device__ __forceinline__ void m_values(uint32_t lo, uint32_t hi, float a, float (&x)[8]) {
+  lo ^= 0x80808080u;  // c + 128
+  hi ^= 0x80808080u;
+  constexpr float less = 8388608.0f + 128.0f;
+#define M4(w, o)                                                                      \
+  x[o] = m_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)) - less, a);     \
+  x[o + 1] = m_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441)) - less, a); \
+  x[o + 2] = m_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)) - less, a); \
+  x[o + 3] = m_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443)) - less, a);
+  M4(lo, 0)
+  M4(hi, 4)
+#undef M4
 }
-__device__ __forceinline__ int v_code(float v, float a) {
-  const float q = rintf(__fmul_rn(__fsqrt_rn(__fsqrt_rn(__fdiv_rn(v, a))), 255.0f));
-  return v > 0.f ? max((int)q, 1) : (int)q;
+__device__ __forceinline__ void v_values(uint32_t lo, uint32_t hi, float a, float (&x)[8]) {
+  constexpr float less = 8388608.0f;
+#define V4(w, o)                                                                      \
+  x[o] = v_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)) - less, a);     \
+  x[o + 1] = v_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441)) - less, a); \
+  x[o + 2] = v_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)) - less, a); \
+  x[o + 3] = v_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443)) - less, a);
+  V4(lo, 0)
+  V4(hi, 4)
+#undef V4
 }
 
+// The nearest code of m / a, of v / a (a > 0): rint(127 sqrt(|m| / a)) and
+// rint(255 sqrt(sqrt(v / a))), every operation correctly rounded.  Those take some
+// 60 instructions an element and would bound the kernel, so the approximate
+// instructions decide first: with 1 / a, the products and the roots each within
+// 2^-23, 127 times the root is off by less than 4e-5 and 255 times the fourth root
+// by less than 1e-4.  Only where one of them lies nearer than 6e-5 or 1.5e-4 to a
+// tie (one element in 2000) both take the exact way.  The limits are negative,
+// for every element to take it, where 1 / a or the quotients could leave the
+// normal numbers.  A code is the low byte of its FP32 value plus 1.5 2^23.
+__device__ __forceinline__ float sqrt_fast(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
+struct Encode {
+  float am, av;     // the block's largest magnitudes
+  float rm, rv;     // 1 / am, 1 / av, or 0
+  float dm, dv;     // limits of the distance from the rounded value
+};
+__device__ __forceinline__ Encode encode_with(float am, float av) {
+  Encode e;
+  e.am = am;
+  e.av = av;
+  const bool fm = am > 1e-30f && am < 1e30f, fv = av > 1e-30f && av < 1e30f;
+  e.rm = fm ? __frcp_rn(am) : 0.f;
+  e.rv = fv ? __frcp_rn(av) : 0.f;
+  // a block of zeros: every code is 0 without a division by 0
+  e.dm = fm ? 0.5f - 6e-5f : am > 0.f ? -1.f : 1.f;
+  e.dv = fv ? 0.5f - 1.5e-4f : av > 0.f ? -1.f : 1.f;
+  return e;
+}
+// Codes in the low bytes of cm and cv.
+__device__ __forceinline__ void codes(const Encode &e, float m, float v, uint32_t &cm,
+                                      uint32_t &cv) {
+  const float x = sqrt_fast(fabsf(m) * e.rm) * 127.0f;
+  const float y = sqrt_fast(sqrt_fast(v * e.rv)) * 255.0f;
+  float p = x + kRound, q = y + kRound;
+  // NaN too; in a block of Inf or NaN the exact way gives what the division gives
+  if (!(fabsf(x - (p - kRound)) <= e.dm) || !(fabsf(y - (q - kRound)) <= e.dv)) {
+    if (e.am > 0.f) p = rintf(__fmul_rn(__fsqrt_rn(__fdiv_rn(fabsf(m), e.am)), 127.0f)) + kRound;
+    if (e.av > 0.f)
+      q = rintf(__fmul_rn(__fsqrt_rn(__fsqrt_rn(__fdiv_rn(v, e.av))), 255.0f)) + kRound;
+  }
+  const uint32_t c = __float_as_uint(p);
+  cm = m < 0.f ? 0u - c : c;
+  cv = max(__float_as_uint(q), 0x4B400000u + (v > 0.f ? 1u : 0u));
+}
+
+// The largest of a warp's non-negative values (whose bits order as they do).
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
 }
 
 template <int PT, int GT, bool Q8>
-__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Tensors ts,
+__global__ void __launch_bounds__(kThreads, Q8 ? 6 : 1) k_adamw(const __grid_constant__ Tensors ts,
                                                     const Step st) {
   using P = typename Elem<PT>::T;
   using G = typename Elem<GT>::T;
@@ -153,11 +222,12 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Tens
   const bool vec = ts.vec[lo >> 5] >> (lo & 31) & 1;
   const long long numel = ts.numel[lo];
   const int lane = threadIdx.x & 31;
-  const long long block = (long long)(blockIdx.x - ts.first[lo]) * (kThreads / 32) + (threadIdx.x >> 5);
+  const long long block = (long long)(blockIdx.x - ts.first[lo]) * kWarps + (threadIdx.x >> 5);
   const long long at = block * kBlock + lane * 8;
   if (block * kBlock >= numel) return;  // the whole warp
   const int n = (int)min(8LL, max(0LL, numel - at));
 
+  // elements past the end are zeros in, and stay zeros: they change no maximum
   P p8[8];
   G g8[8];
   P *pp = static_cast<P *>(ts.p[lo]) + at;
@@ -168,73 +238,101 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Tens
     load8(static_cast<const float *>(ts.m[lo]) + at, m, n, vec);
     load8(static_cast<const float *>(ts.v[lo]) + at, v, n, vec);
   } else {
-    int8_t cm[8];
-    uint8_t cv[8];
-    load8(static_cast<const int8_t *>(ts.m[lo]) + at, cm, n, vec);
-    load8(static_cast<const uint8_t *>(ts.v[lo]) + at, cv, n, vec);
-    const float am = ts.ms[lo][block], av = ts.vs[lo][block];
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-      m[i] = m_value(cm[i], am);
-      v[i] = v_value(cv[i], av);
-    }
+    union {
+      uint8_t b[8];
+      uint32_t w[2];
+    } cm, cv;
+    load8(static_cast<const uint8_t *>(ts.m[lo]) + at, cm.b, n, vec);
+    load8(static_cast<const uint8_t *>(ts.v[lo]) + at, cv.b, n, vec);
+    m_values(cm.w[0], cm.w[1], ts.ms[lo][block], m);
+    v_values(cv.w[0], cv.w[1], ts.vs[lo][block], v);
   }
+  float am = 0.f, av = 0.f;  // the block's largest magnitudes
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     const float g = Elem<GT>::get(g8[i]);
     m[i] = __fadd_rn(__fmul_rn(m[i], st.b1), __fmul_rn(g, st.one_b1));
     v[i] = __fadd_rn(__fmul_rn(v[i], st.b2), __fmul_rn(__fmul_rn(g, g), st.one_b2));
-    const float d = sqrtf(v[i] * st.c2) + st.eps;
+    const float d = sqrt_fast(v[i] * st.c2) + st.eps;  // 2^-22 of the update
     p8[i] = Elem<PT>::put(Elem<PT>::get(p8[i]) * st.decay - __fdividef(m[i] * st.lr_c1, d));
+    if (Q8) {
+      am = fmaxf(am, fabsf(m[i]));
+      av = fmaxf(av, v[i]);
+    }
   }
   store8(pp, p8, n, vec);
   if (!Q8) {
     store8(static_cast<float *>(ts.m[lo]) + at, m, n, vec);
     store8(static_cast<float *>(ts.v[lo]) + at, v, n, vec);
   } else {
-    float am = 0.f, av = 0.f;
+    const Encode e = encode_with(warp_max(am), warp_max(av));
+    union {
+      uint8_t b[8];
+      uint32_t w[2];
+    } cm, cv;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      am = fmaxf(am, i < n ? fabsf(m[i]) : 0.f);
-      av = fmaxf(av, i < n ? v[i] : 0.f);
-    }
-    am = warp_max(am);
-    av = warp_max(av);
-    int8_t cm[8];
-    uint8_t cv[8];
+    for (int h = 0; h < 2; h++) {
+      uint32_t x[4], y[4];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      cm[i] = am > 0.f ? (int8_t)m_code(m[i], am) : 0;
-      cv[i] = av > 0.f ? (uint8_t)v_code(v[i], av) : 0;
+      for (int i = 0; i < 4; i++) codes(e, m[4 * h + i], v[4 * h + i], x[i], y[i]);
+      cm.w[h] = __byte_perm(__byte_perm(x[0], x[1], 0x0040), __byte_perm(x[2], x[3], 0x0040), 0x5410);
+      cv.w[h] = __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
     }
-    store8(static_cast<int8_t *>(ts.m[lo]) + at, cm, n, vec);
-    store8(static_cast<uint8_t *>(ts.v[lo]) + at, cv, n, vec);
+    store8(static_cast<uint8_t *>(ts.m[lo]) + at, cm.b, n, vec);
+    store8(static_cast<uint8_t *>(ts.v[lo]) + at, cv.b, n, vec);
     if (lane == 0) {
-      ts.ms[lo][block] = am;
-      ts.vs[lo][block] = av;
+      ts.ms[lo][block] = e.am;
+      ts.vs[lo][block] = e.av;
     }
   }
 }
 
+// Four consecutive elements a lane and run, so that a store instruction covers
+// whole lines; four runs in flight.
+constexpr int kMomentRuns = 4;
 __global__ void __launch_bounds__(kThreads)
     k_moments(long long numel, const int8_t *cm, const float *am, const uint8_t *cv,
               const float *av, float *m, float *v, bool vec) {
-  const long long at = ((long long)blockIdx.x * kThreads + threadIdx.x) * 8;
-  if (at >= numel) return;
-  const int n = (int)min(8LL, numel - at);
-  int8_t a[8];
-  uint8_t b[8];
-  load8(cm + at, a, n, vec);
-  load8(cv + at, b, n, vec);
-  const float sa = am[at / kBlock], sb = av[at / kBlock];
-  float x[8], y[8];
+  const long long base = (long long)blockIdx.x * kThreads * 4 * kMomentRuns + threadIdx.x * 4;
+  uint32_t a[kMomentRuns], b[kMomentRuns];
+  float sa[kMomentRuns], sb[kMomentRuns];
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    x[i] = m_value(a[i], sa);
-    y[i] = v_value(b[i], sb);
+  for (int r = 0; r < kMomentRuns; r++) {
+    const long long at = base + (long long)r * kThreads * 4;
+    a[r] = b[r] = 0;
+    sa[r] = sb[r] = 0.f;
+    if (at < numel) {
+      sa[r] = am[at / kBlock];
+      sb[r] = av[at / kBlock];
+      if (vec && at + 4 <= numel) {
+        a[r] = *reinterpret_cast<const uint32_t *>(cm + at);
+        b[r] = *reinterpret_cast<const uint32_t *>(cv + at);
+      } else {
+        for (int i = 0; i < 4 && at + i < numel; i++) {
+          a[r] |= (uint32_t)(uint8_t)cm[at + i] << (8 * i);
+          b[r] |= (uint32_t)cv[at + i] << (8 * i);
+        }
+      }
+    }
   }
-  store8(m + at, x, n, vec);
-  store8(v + at, y, n, vec);
+#pragma unroll
+  for (int r = 0; r < kMomentRuns; r++) {
+    const long long at = base + (long long)r * kThreads * 4;
+    float x[8], y[8];  // the last four are not used
+    m_values(a[r], 0, sa[r], x);
+    v_values(b[r], 0, sb[r], y);
+    if (vec && at + 4 <= numel) {
+      *reinterpret_cast<float4 *>(m + at) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4 *>(v + at) = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (at + i < numel) {
+          m[at + i] = x[i];
+          v[at + i] = y[i];
+        }
+    }
+  }
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -343,8 +441,9 @@ extern "C" os2_status os2_adamw_moments(long long numel, const int8_t *exp_avg,
       !aligned(v, 4))
     return OS2_ERR_INVALID_ARG;
   if (numel > (1LL << 40)) return OS2_ERR_UNSUPPORTED;
-  const bool vec = aligned(exp_avg, 8) && aligned(exp_avg_sq, 8) && aligned(m, 16) && aligned(v, 16);
-  const unsigned grid = (unsigned)((numel + kChunk - 1) / kChunk);
+  const bool vec = aligned(exp_avg, 4) && aligned(exp_avg_sq, 4) && aligned(m, 16) && aligned(v, 16);
+  constexpr long long per = kThreads * 4 * kMomentRuns;
+  const unsigned grid = (unsigned)((numel + per - 1) / per);
   k_moments<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
       numel, exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, m, v, vec);
   return cudaGetLastError() == cudaSuccess ? OS2_OK : OS2_ERR_CUDA;

@@ -22,8 +22,6 @@
 // for the one in front of it on the stream, which quantises the tokens: they are
 // inputs of the call, and nothing in front of that kernel can be writing them
 // still.  Every wait is bounded, as in mm2.cuh.
-#include <limits.h>
-
 #include "i8.cuh"
 
 using namespace os2i8;
@@ -322,17 +320,22 @@ cudaError_t launch(const I8Args &a, cudaStream_t s) {
   j.n = a.n;
   j.tiles = (a.n + 127) / 128;
   j.stages = (a.k + kStageK - 1) / kStageK;
-  // the cluster size whose busiest CTA has the fewest stages; a larger one has to
-  // save more than one
-  long least = LONG_MAX;
+  // The cluster size by an estimate in microseconds: a stage takes a CTA 0.19 (what
+  // its SM can take in), or 0.0026 for each CTA that streams at the same time
+  // (memory); a tile's end takes 0.3, and 1.0 more where parts are joined.
+  double least = 1e30;
   for (const int c : {1, 2, 4, 8}) {
     if (c > j.stages) break;
-    const int n = std::min(clusters_of<NG>(c), j.tiles);
-    const long t = (long)((j.tiles + n - 1) / n) * ((j.stages + c - 1) / c) + 1;
+    const int most = std::min(clusters_of<NG>(c), j.tiles), per = (j.stages + c - 1) / c;
+    auto wave = [&](int clusters) {
+      return per * std::max(0.19, 0.0026 * clusters * c) + (c > 1 ? 1.3 : 0.3);
+    };
+    const int rest = j.tiles % most;
+    const double t = (j.tiles / most) * wave(most) + (rest ? wave(rest) : 0.);
     if (t < least) {
-      least = t - 1;
+      least = t;
       j.cluster = c;
-      j.clusters = n;
+      j.clusters = most;
     }
   }
   CUtensorMap mw, mt;

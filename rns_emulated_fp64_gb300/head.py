@@ -18,9 +18,10 @@ import ctypes as ct
 
 import torch
 
-from .binding import _check, _stream, alloc_workspace, load
+from .binding import _check, load
 
 F32, F16, BF16 = 0, 1, 2
+_INT8, _HALVES = (torch.int8,), (torch.bfloat16, torch.float16)
 _DTYPE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 ADAMW_BLOCK = 256  # elements that share a scale of an 8-bit moment
 
@@ -28,54 +29,61 @@ ADAMW_BLOCK = 256  # elements that share a scale of an 8-bit moment
 _HERE = contextlib.nullcontext()
 
 
-def _on(device, stream):
+def _on(index, stream):
     """Device and stream of a call; what it allocates and copies belongs to them."""
     if stream is None:
-        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=index)
     return torch.cuda.stream(stream)
 
 
+# the current stream's handle, without a Stream object around it (3 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _rows(X, name, dtypes):
-    """A 2-D CUDA tensor with contiguous rows; returns its leading dimension."""
-    if not (X.is_cuda and X.dim() == 2 and X.dtype in dtypes):
+    """Checks a 2-D CUDA tensor with contiguous rows; returns (rows, columns,
+    leading dimension)."""
+    if X.dim() != 2 or X.dtype not in dtypes or not X.is_cuda:
         raise ValueError(f"{name} must be a 2-D CUDA tensor of " + ", ".join(str(t) for t in dtypes))
-    if X.shape[1] > 1 and X.stride(1) != 1:
+    (m, k), (ld, inner) = X.shape, X.stride()
+    if inner != 1 and k > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return _ld(X)
-
-
-def _ld(X):
     # the stride of a single row means nothing
-    return max(X.stride(0) if X.shape[0] > 1 else 0, X.shape[1], 1)
+    return m, k, (ld if m > 1 and ld > k else k if k else 1)
 
 
-def _vector(x, name, n, dtype, device):
-    if x.dtype != dtype or x.device != device or x.dim() != 1 or x.shape[0] != n:
-        raise ValueError(f"{name} must be {n} {dtype} values on {device}")
+def _vector(x, name, n, dtype, index):
+    if x.dtype is not dtype or x.dim() != 1 or x.shape[0] != n or x.get_device() != index:
+        raise ValueError(f"{name} must be {n} {dtype} values on cuda:{index}")
     return x if x.is_contiguous() else x.contiguous()
 
 
-def _out(out, shape, dtype, device, name="out"):
+def _out(out, like, shape, dtype, name="out"):
+    """The output and its leading dimension."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
-        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {device}")
-    if out.dim() == 2 and out.shape[1] > 1 and out.stride(1) != 1:
+        return torch.empty(shape, dtype=dtype, device=like.device), shape[-1] or 1
+    if tuple(out.shape) != shape or out.dtype is not dtype or out.device != like.device:
+        raise ValueError(f"{name} must be {shape} {dtype} on {like.device}")
+    if len(shape) == 1:
+        if not out.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return out, shape[0]
+    if shape[1] > 1 and out.stride(1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if out.dim() == 2 and out.shape[0] > 1 and out.stride(0) < out.shape[1]:
+    if shape[0] > 1 and out.stride(0) < shape[1]:
         raise ValueError(f"{name} must not overlap itself")
-    if out.dim() == 1 and not out.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return out
+    return out, max(out.stride(0) if shape[0] > 1 else 0, shape[1], 1)
 
 
-def _workspace(workspace, need, device):
+def _workspace(workspace, need, like):
+    """The workspace's address and size (a new one stays alive in the caller)."""
     if workspace is None:
-        return alloc_workspace(need, device)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {device}")
+        return torch.empty(need or 1, dtype=torch.uint8, device=like.device)
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {like.device}")
     return workspace
 
 
@@ -88,42 +96,40 @@ def quantize_rows(X: torch.Tensor, out=None, scale=None, stream=None):
     """8-bit integers of X (m x k, float32, float16 or bfloat16) with one scale
     a row: returns (q int8, scale float32), X ~ q * scale[:, None].  Weights are
     quantised by output channel the same way, as n x k."""
-    ld = _rows(X, "X", tuple(_DTYPE))
-    m, k = X.shape
-    with _on(X.device, stream):
-        q = _out(out, (m, k), torch.int8, X.device)
-        scale = _out(scale, (m,), torch.float32, X.device, "scale")
-        _check(load().os2_quantize_rows(m, k, _DTYPE[X.dtype], X.data_ptr(), ld, q.data_ptr(),
-                                        _ld(q), scale.data_ptr(), _stream(None)),
-               "os2_quantize_rows")
+    m, k, ld = _rows(X, "X", _DTYPE)
+    index = X.get_device()
+    with _on(index, stream):
+        q, ldq = _out(out, X, (m, k), torch.int8)
+        scale, _ = _out(scale, X, (m,), torch.float32, "scale")
+        _check(load().os2_quantize_rows(m, k, _DTYPE[X.dtype], X.data_ptr(), ld, q.data_ptr(), ldq,
+                                        scale.data_ptr(), _raw_stream(index)), "os2_quantize_rows")
     return q, scale
 
 
-def _i8(X, ldx, a_scale, Bt, b_scale, bias, out_dtype, out, workspace, stream):
-    ldb = _rows(Bt, "Bt", (torch.int8,))
-    m, k = X.shape
-    n = Bt.shape[0]
-    dev = X.device
-    if Bt.device != dev:
-        raise ValueError(f"Bt must be on {dev}")
-    if Bt.shape[1] != k:
+def _i8(X, m, k, ldx, a_scale, Bt, b_scale, bias, out_dtype, out, workspace, stream):
+    n, kb, ldb = _rows(Bt, "Bt", _INT8)
+    index = X.get_device()
+    if Bt.get_device() != index:
+        raise ValueError(f"Bt must be on {X.device}")
+    if kb != k:
         raise ValueError("inner dimensions differ")
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
     if out_dtype not in _DTYPE:
         raise ValueError("out_dtype must be float32, float16 or bfloat16")
     L = load()
-    with _on(dev, stream):
+    with _on(index, stream):
         if a_scale is not None:
-            a_scale = _vector(a_scale, "a_scale", m, torch.float32, dev)
-        b_scale = _vector(b_scale, "b_scale", n, torch.float32, dev)
+            a_scale = _vector(a_scale, "a_scale", m, torch.float32, index)
+        b_scale = _vector(b_scale, "b_scale", n, torch.float32, index)
         if bias is not None:
-            bias = _vector(bias, "bias", n, torch.float32, dev)
-        out = _out(out, (m, n), out_dtype, dev)
-        ws = _workspace(workspace, L.os2_i8gemm_workspace_size(m, n, k, Bt.data_ptr(), ldb), dev)
-        rest = (Bt.data_ptr(), ldb, b_scale.data_ptr(), None if bias is None else bias.data_ptr(),
-                out.data_ptr(), _ld(out), _DTYPE[out_dtype], ws.data_ptr(), _nbytes(ws),
-                _stream(None))
+            bias = _vector(bias, "bias", n, torch.float32, index)
+        out, ldc = _out(out, X, (m, n), out_dtype)
+        bp = Bt.data_ptr()
+        ws = _workspace(workspace, L.os2_i8gemm_workspace_size(m, n, k, bp, ldb), X)
+        rest = (bp, ldb, b_scale.data_ptr(), None if bias is None else bias.data_ptr(),
+                out.data_ptr(), ldc, _DTYPE[out_dtype], ws.data_ptr(), _nbytes(ws),
+                _raw_stream(index))
         if a_scale is not None:
             _check(L.os2_i8gemm(m, n, k, X.data_ptr(), ldx, a_scale.data_ptr(), *rest),
                    "os2_i8gemm")
@@ -139,8 +145,10 @@ def i8gemm(A: torch.Tensor, a_scale: torch.Tensor, Bt: torch.Tensor, b_scale: to
 
     A: m x k int8 (tokens), Bt: n x k int8 (output channels), scales and bias
     float32.  out_dtype: float32, float16 or bfloat16 (the default)."""
-    lda = _rows(A, "A", (torch.int8,))
-    return _i8(A, lda, a_scale, Bt, b_scale, bias, out_dtype, out, workspace, stream)
+    m, k, lda = _rows(A, "A", _INT8)
+    if a_scale is None:
+        raise ValueError("a_scale is missing")
+    return _i8(A, m, k, lda, a_scale, Bt, b_scale, bias, out_dtype, out, workspace, stream)
 
 
 def i8linear(X: torch.Tensor, Bt: torch.Tensor, b_scale: torch.Tensor, bias=None, out_dtype=None,
@@ -148,20 +156,22 @@ def i8linear(X: torch.Tensor, Bt: torch.Tensor, b_scale: torch.Tensor, bias=None
     """A linear layer with 8-bit weights: X (m x k, float32, float16 or
     bfloat16) is quantised token by token (``quantize_rows``), then ``i8gemm``.
     out_dtype: X's by default."""
-    ldx = _rows(X, "X", tuple(_DTYPE))
+    m, k, ldx = _rows(X, "X", _DTYPE)
     if out_dtype is None and out is None:
         out_dtype = X.dtype
-    return _i8(X, ldx, None, Bt, b_scale, bias, out_dtype, out, workspace, stream)
+    return _i8(X, m, k, ldx, None, Bt, b_scale, bias, out_dtype, out, workspace, stream)
 
 
 # ------------------------------------------------------------ cross entropy
 def _head(H, W):
-    ldh, ldw = _rows(H, "H", (torch.bfloat16, torch.float16)), _rows(W, "W", (H.dtype,))
-    if W.device != H.device:
+    n, k, ldh = _rows(H, "H", _HALVES)
+    v, kw, ldw = _rows(W, "W", (H.dtype,))
+    index = H.get_device()
+    if W.get_device() != index:
         raise ValueError(f"W must be on {H.device}")
-    if H.shape[1] != W.shape[1]:
+    if kw != k:
         raise ValueError("inner dimensions differ")
-    return ldh, ldw
+    return n, k, v, ldh, ldw, index
 
 
 def xent(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, ignore_index: int = -100,
@@ -171,17 +181,18 @@ def xent(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, ignore_index: i
     H: n x k, W: v x k, bfloat16 or float16; labels: n int64.  Returns (loss,
     lse), float32, one value a row; 0 for rows labelled ignore_index.  A label
     out of range is reported by ``get_status`` (ERR_RANGE)."""
-    ldh, ldw = _head(H, W)
-    (n, k), v, dev = H.shape, W.shape[0], H.device
+    n, k, v, ldh, ldw, index = _head(H, W)
     L = load()
-    with _on(dev, stream):
-        labels = _vector(labels, "labels", n, torch.int64, dev)
+    with _on(index, stream):
+        labels = _vector(labels, "labels", n, torch.int64, index)
+        dev = H.device
         loss = torch.empty(n, dtype=torch.float32, device=dev)
         lse = torch.empty(n, dtype=torch.float32, device=dev)
-        ws = _workspace(workspace, L.os2_xent_workspace_size(n, k, v, W.data_ptr(), ldw, 0), dev)
-        _check(L.os2_xent(n, k, v, _DTYPE[H.dtype], H.data_ptr(), ldh, W.data_ptr(), ldw,
-                          labels.data_ptr(), int(ignore_index), loss.data_ptr(), lse.data_ptr(),
-                          ws.data_ptr(), _nbytes(ws), _stream(None)), "os2_xent")
+        wp = W.data_ptr()
+        ws = _workspace(workspace, L.os2_xent_workspace_size(n, k, v, wp, ldw, 0), H)
+        _check(L.os2_xent(n, k, v, _DTYPE[H.dtype], H.data_ptr(), ldh, wp, ldw, labels.data_ptr(),
+                          int(ignore_index), loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+                          _nbytes(ws), _raw_stream(index)), "os2_xent")
     return loss, lse
 
 
@@ -190,21 +201,22 @@ def xent_backward(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, lse: t
                   need_dw: bool = True, workspace=None, stream=None):
     """The gradient of ``xent``: (dH, dW) for grad = d/d loss (n float32 values),
     in H's type; None for the one not needed."""
-    ldh, ldw = _head(H, W)
-    (n, k), v, dev = H.shape, W.shape[0], H.device
+    n, k, v, ldh, ldw, index = _head(H, W)
     L = load()
-    with _on(dev, stream):
-        labels = _vector(labels, "labels", n, torch.int64, dev)
-        lse = _vector(lse, "lse", n, torch.float32, dev)
-        grad = _vector(grad, "grad", n, torch.float32, dev)
-        dh = torch.empty((n, k), dtype=H.dtype, device=dev) if need_dh else None
-        dw = torch.empty((v, k), dtype=H.dtype, device=dev) if need_dw else None
-        ws = _workspace(workspace, L.os2_xent_workspace_size(n, k, v, W.data_ptr(), ldw, 1), dev)
-        _check(L.os2_xent_backward(n, k, v, _DTYPE[H.dtype], H.data_ptr(), ldh, W.data_ptr(), ldw,
+    with _on(index, stream):
+        labels = _vector(labels, "labels", n, torch.int64, index)
+        lse = _vector(lse, "lse", n, torch.float32, index)
+        grad = _vector(grad, "grad", n, torch.float32, index)
+        dt, dev = H.dtype, H.device
+        dh = torch.empty((n, k), dtype=dt, device=dev) if need_dh else None
+        dw = torch.empty((v, k), dtype=dt, device=dev) if need_dw else None
+        wp = W.data_ptr()
+        ws = _workspace(workspace, L.os2_xent_workspace_size(n, k, v, wp, ldw, 1), H)
+        _check(L.os2_xent_backward(n, k, v, _DTYPE[H.dtype], H.data_ptr(), ldh, wp, ldw,
                                    labels.data_ptr(), int(ignore_index), lse.data_ptr(),
                                    grad.data_ptr(), None if dh is None else dh.data_ptr(), k,
                                    None if dw is None else dw.data_ptr(), k, ws.data_ptr(),
-                                   _nbytes(ws), _stream(None)), "os2_xent_backward")
+                                   _nbytes(ws), _raw_stream(index)), "os2_xent_backward")
     return dh, dw
 
 
@@ -232,15 +244,19 @@ def _pointers(ts):
     return (ct.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
 
 
-def _list(ts, name, like, dtypes):
-    if len(ts) != len(like):
-        raise ValueError(f"{name}: {len(ts)} tensors for {len(like)} parameters")
+def _list(ts, name, shapes, index, dtypes):
+    """Checks a list of tensors, one for each parameter; returns their type."""
+    if len(ts) != len(shapes):
+        raise ValueError(f"{name}: {len(ts)} tensors for {len(shapes)} parameters")
     dtype = ts[0].dtype
     if dtype not in dtypes:
         raise ValueError(f"{name} must be " + " or ".join(str(t) for t in dtypes))
-    for t, p in zip(ts, like):
-        if t.dtype != dtype or t.device != p.device or t.shape != p.shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous, of one type, and match the parameters")
+    for t, shape in zip(ts, shapes):
+        if (t.shape != shape or t.dtype is not dtype or t.get_device() != index or
+                not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous, of one type, on one CUDA device, and "
+                             "match the parameters")
+    return dtype
 
 
 def adamw(params, grads, exp_avg, exp_avg_sq, *, step: int, lr: float, beta1: float = 0.9,
@@ -254,14 +270,15 @@ def adamw(params, grads, exp_avg, exp_avg_sq, *, step: int, lr: float, beta1: fl
     params = list(params)
     if not params:
         return
-    dev = params[0].device
-    if dev.type != "cuda" or any(p.device != dev for p in params):
+    index = params[0].get_device()
+    if index < 0:
         raise ValueError("params must be on one CUDA device")
-    _list(params, "params", params, tuple(_DTYPE))
-    _list(grads, "grads", params, tuple(_DTYPE))
+    shapes = [p.shape for p in params]
+    pt = _list(params, "params", shapes, index, _DTYPE)
+    gt = _list(grads, "grads", shapes, index, _DTYPE)
     q8 = exp_avg_scales is not None or exp_avg_sq_scales is not None
-    _list(exp_avg, "exp_avg", params, (torch.int8,) if q8 else (torch.float32,))
-    _list(exp_avg_sq, "exp_avg_sq", params, (torch.uint8,) if q8 else (torch.float32,))
+    _list(exp_avg, "exp_avg", shapes, index, _INT8 if q8 else (torch.float32,))
+    _list(exp_avg_sq, "exp_avg_sq", shapes, index, (torch.uint8,) if q8 else (torch.float32,))
     sizes = [p.numel() for p in params]
     scales = (None, None)
     if q8:
@@ -269,17 +286,17 @@ def adamw(params, grads, exp_avg, exp_avg_sq, *, step: int, lr: float, beta1: fl
             if ss is None or len(ss) != len(params):
                 raise ValueError(f"{name}: one tensor for each parameter")
             for s, n in zip(ss, sizes):
-                if (s.dtype != torch.float32 or s.device != dev or not s.is_contiguous() or
-                        s.numel() != -(-n // ADAMW_BLOCK)):
+                if (s.dtype is not torch.float32 or s.get_device() != index or
+                        not s.is_contiguous() or s.numel() != -(-n // ADAMW_BLOCK)):
                     raise ValueError(f"{name} must be contiguous float32, one value for each "
                                      f"{ADAMW_BLOCK} elements")
         scales = _pointers(exp_avg_scales), _pointers(exp_avg_sq_scales)
-    with _on(dev, stream):
+    with _on(index, stream):
         _check(load().os2_adamw(len(params), (ct.c_longlong * len(params))(*sizes),
                                 _pointers(params), _pointers(grads), _pointers(exp_avg),
-                                _pointers(exp_avg_sq), *scales, _DTYPE[params[0].dtype],
-                                _DTYPE[grads[0].dtype], 8 if q8 else 32, lr, beta1, beta2, eps,
-                                weight_decay, int(step), _stream(None)), "os2_adamw")
+                                _pointers(exp_avg_sq), *scales, _DTYPE[pt], _DTYPE[gt],
+                                8 if q8 else 32, lr, beta1, beta2, eps, weight_decay, int(step),
+                                _raw_stream(index)), "os2_adamw")
 
 
 def adamw_moments(exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, stream=None):
@@ -292,11 +309,12 @@ def adamw_moments(exp_avg, exp_avg_scale, exp_avg_sq, exp_avg_sq_scale, stream=N
                                  (exp_avg_sq_scale, "exp_avg_sq_scale", torch.float32, -(-n // ADAMW_BLOCK))):
         if not t.is_cuda or t.device != exp_avg.device or t.dtype != dtype or t.numel() != size or not t.is_contiguous():
             raise ValueError(f"{name} must be {size} contiguous {dtype} values on one CUDA device")
-    with _on(exp_avg.device, stream):
+    index = exp_avg.get_device()
+    with _on(index, stream):
         m = torch.empty(exp_avg.shape, dtype=torch.float32, device=exp_avg.device)
         v = torch.empty_like(m)
         _check(load().os2_adamw_moments(n, exp_avg.data_ptr(), exp_avg_scale.data_ptr(),
                                         exp_avg_sq.data_ptr(), exp_avg_sq_scale.data_ptr(),
-                                        m.data_ptr(), v.data_ptr(), _stream(None)),
+                                        m.data_ptr(), v.data_ptr(), _raw_stream(index)),
                "os2_adamw_moments")
     return m, v

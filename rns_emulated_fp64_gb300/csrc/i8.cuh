@@ -189,4 +189,40 @@ inline bool map_w(CUtensorMap *map, const void *base, long k, long rows, long pi
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// ------------------------------------------------ streams in clusters (host)
+// The cluster size of a streaming kernel (k_i8few.cu, k_xent_few.cu) for `tiles`
+// tiles of `stages` 16 KB stages, by an estimate in microseconds: a stage takes a
+// CTA 0.19 (what its SM can take in), or 0.0026 for each CTA that streams at the same
+// time (memory); a tile's end takes 0.3, and 1.0 more where parts are joined.
+void few_clusters(const void *kernel, int threads, size_t smem, int tiles, int stages,
+                  int *cluster, int *clusters);
+
+// Launches a kernel in clusters of `cluster` CTAs; overlap: before the kernel in
+// front of it on the stream has ended (it waits for that itself).
+template <class... P, class... A>
+cudaError_t launch_cluster(void (*kernel)(P...), int cluster, int grid, int block, size_t smem,
+                           bool overlap, cudaStream_t s, const A &...args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+
 }  // namespace os2i8

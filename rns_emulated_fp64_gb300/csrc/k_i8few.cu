@@ -22,6 +22,8 @@
 // for the one in front of it on the stream, which quantises the tokens: they are
 // inputs of the call, and nothing in front of that kernel can be writing them
 // still.  Every wait is bounded, as in mm2.cuh.
+#include <map>
+
 #include "i8.cuh"
 
 using namespace os2i8;
@@ -48,14 +50,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-
 struct FewJob {
   int m, n, tiles, stages;
   int cluster, clusters;     // CTAs of a cluster (1, 2, 4 or 8), clusters of the grid
@@ -119,7 +113,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       int i = 0;
       for (int t = first; t < j.tiles && i < F::stages; t += j.clusters)
         for (int ks = s0; ks < s1 && i < F::stages; ks++) weights(i++, t, ks);
-      asm volatile("griddepcontrol.wait;" ::: "memory");
+      wait_for_previous();
       int st = 0;
       uint32_t ph = 0, used = 0, last_par = 0;
       bool ok = true;
@@ -224,7 +218,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       }
       if (!ok) break;
       if (!waited) {  // the tokens' scales and the output; the other CTAs' barriers
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        wait_for_previous();
         cluster_wait();
         waited = true;
       }
@@ -282,29 +276,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   cluster_sync();
 }
 
-// Clusters of c CTAs that run at once on the device.
-template <int NG>
-int clusters_of(int c) {
-  static std::mutex mu;
-  static int known[9] = {};
-  std::lock_guard<std::mutex> g(mu);
-  if (!known[c]) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim = {(unsigned)c, 1, 1};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(os2_sm_count() / c * c));
-    cfg.blockDim = dim3(kFewThreads);
-    cfg.dynamicSmemBytes = Few<NG>::smem;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int v = 0;
-    if (cudaOccupancyMaxActiveClusters(&v, k_i8few<NG>, &cfg) != cudaSuccess) v = 0;
-    known[c] = std::max(1, std::min(v, os2_sm_count() / c));
-  }
-  return known[c];
-}
-
 template <int NG>
 cudaError_t launch(const I8Args &a, cudaStream_t s) {
   using F = Few<NG>;
@@ -320,24 +291,8 @@ cudaError_t launch(const I8Args &a, cudaStream_t s) {
   j.n = a.n;
   j.tiles = (a.n + 127) / 128;
   j.stages = (a.k + kStageK - 1) / kStageK;
-  // The cluster size by an estimate in microseconds: a stage takes a CTA 0.19 (what
-  // its SM can take in), or 0.0026 for each CTA that streams at the same time
-  // (memory); a tile's end takes 0.3, and 1.0 more where parts are joined.
-  double least = 1e30;
-  for (const int c : {1, 2, 4, 8}) {
-    if (c > j.stages) break;
-    const int most = std::min(clusters_of<NG>(c), j.tiles), per = (j.stages + c - 1) / c;
-    auto wave = [&](int clusters) {
-      return per * std::max(0.19, 0.0026 * clusters * c) + (c > 1 ? 1.3 : 0.3);
-    };
-    const int rest = j.tiles % most;
-    const double t = (j.tiles / most) * wave(most) + (rest ? wave(rest) : 0.);
-    if (t < least) {
-      least = t;
-      j.cluster = c;
-      j.clusters = most;
-    }
-  }
+  few_clusters(reinterpret_cast<const void *>(k_i8few<NG>), kFewThreads, F::smem, j.tiles, j.stages,
+               &j.cluster, &j.clusters);
   CUtensorMap mw, mt;
   if (!map_w(&mw, a.W, a.k, a.n, a.ldw) ||
       !make_map(&mt, a.tokens, false, a.k, a.m, a.pitch, false, NG * 8))
@@ -348,19 +303,8 @@ cudaError_t launch(const I8Args &a, cudaStream_t s) {
   j.bias = a.bias;
   j.y = a.y;
   j.ldy = a.ldy;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {(unsigned)j.cluster, 1, 1};
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(j.cluster * j.clusters));
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = F::smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.overlap ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_i8few<NG>, mw, mt, j, a.status);
+  return launch_cluster(k_i8few<NG>, j.cluster, j.cluster * j.clusters, kFewThreads, F::smem,
+                        a.overlap, s, mw, mt, j, a.status);
 }
 
 int groups(int m) { return m <= 8 ? 1 : m <= 16 ? 2 : 4; }
@@ -370,4 +314,51 @@ int groups(int m) { return m <= 8 ? 1 : m <= 16 ? 2 : 4; }
 cudaError_t launch_i8few(const I8Args &a, cudaStream_t s) {
   const int g = groups(a.m);
   return g == 1 ? launch<1>(a, s) : g == 2 ? launch<2>(a, s) : launch<4>(a, s);
+}
+
+// ------------------------------------------------------------- cluster sizes
+namespace {
+
+// Clusters of c CTAs of a kernel that run at once on the device.
+int resident_clusters(const void *kernel, int threads, size_t smem, int c) {
+  static std::mutex mu;
+  static std::map<std::pair<const void *, int>, int> known;
+  std::lock_guard<std::mutex> g(mu);
+  int &n = known[{kernel, c}];
+  if (!n) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {(unsigned)c, 1, 1};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(os2_sm_count() / c * c));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int v = 0;
+    if (cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess) v = 0;
+    n = std::max(1, std::min(v, os2_sm_count() / c));
+  }
+  return n;
+}
+
+}  // namespace
+
+void os2i8::few_clusters(const void *kernel, int threads, size_t smem, int tiles, int stages,
+                         int *cluster, int *clusters) {
+  double least = 1e30;
+  for (const int c : {1, 2, 4, 8}) {
+    if (c > stages) break;
+    const int most = std::min(resident_clusters(kernel, threads, smem, c), tiles);
+    const int per = (stages + c - 1) / c, rest = tiles % most;
+    auto wave = [&](int n) {
+      return per * std::max(0.19, 0.0026 * n * c) + (c > 1 ? 1.3 : 0.3);
+    };
+    const double t = (tiles / most) * wave(most) + (rest ? wave(rest) : 0.);
+    if (t < least) {
+      least = t;
+      *cluster = c;
+      *clusters = most;
+    }
+  }
 }

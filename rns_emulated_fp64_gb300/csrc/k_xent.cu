@@ -14,26 +14,19 @@
 // then D W (added in FP32 over the pieces) and D^T H, which take W, D and H as
 // they lie (MN-major operands: nothing is transposed in memory).
 // The tensor cores bound all three products for more than some 300 rows (2 n
-// flop a byte of W), the weights' bytes below that.
-#include "mm2.cuh"
+// flop a byte of W), the weights' bytes below that.  Up to 32 rows the forward pass
+// is a stream of W (k_xent_few.cu).
+#include "xent.cuh"
 
 using namespace os2mm;
+using namespace os2xent;
 
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 // Powers of two that the logits' gradients are held times: |d| <= 2^14 in FP16
 // and 2^40 in BF16, so that a probability keeps its full precision down to
 // 2^-28 and 2^-166 and vanishes below 2^-38 and 2^-173.
 constexpr int kGradExp16 = 14, kGradExpB = 40;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -88,6 +81,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_xent_prep(const Prep p) {
   __shared__ int s_pos[kPrepThreads], s_warp[kPrepThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r0 = blockIdx.x * p.rows_cta, r1 = min(p.n, r0 + p.rows_cta);
+  next_may_start();
   if (tid < 2) s_sum[tid] = 0;
   __syncthreads();
   int before = 0, total = 0;
@@ -186,55 +180,85 @@ __global__ void __launch_bounds__(kPrepThreads) k_xent_prep(const Prep p) {
 
 // W's rows at a pitch and base that TMA takes (only where W's own are not)
 __global__ void k_repack(const uint16_t *src, long ld, uint16_t *dst, long pitch, int rows, int k) {
+  next_may_start();
+  wait_for_previous();
   for (long r = blockIdx.x; r < rows; r += gridDim.x)
     for (int h = threadIdx.x; h < k; h += blockDim.x) dst[r * pitch + h] = src[r * ld + h];
 }
 
 // ------------------------------------------------------------ epilogues
 // Forward: maximum (times log2 e) and sum of exponentials of 128 columns.
+// CHUNKED (k > 1024): the tensor cores' sums, which lose up to 2^-23 a step, are
+// added up in registers every 1024 terms: lse and loss are 4e-7 off at any k,
+// instead of 1.6e-6 at 4096 and 3.3e-6 at 8192, for no time (the epilogue runs
+// beside the next chunk's MMAs).
+template <bool CHUNKED>
 struct StatsEpi {
   const int *label;
   float *zlabel;
   float2 *part;   // [rows][parts]
   int parts, v;
+  float z[CHUNKED ? 8 : 1][16];
 
-  __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, int, int m,
-                                       int *status) {
+  // N columns' logits x, `left` of which exist; y: the label's place among them
+  template <int N>
+  __device__ __forceinline__ void group(const float (&x)[N], int left, int y, int row, float &top,
+                                        float &sum) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; i++) mx = fmaxf(mx, i < left ? x[i] : -INFINITY);
+    const float t = fmaxf(top, mx * kLog2e);
+    // a row of -inf so far: exponents against 0 (every term is 0)
+    const float t0 = t == -INFINITY ? 0.f : t;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      s0 += i < left ? ex2(fmaf(x[i], kLog2e, -t0)) : 0.f;
+      s1 += i + 1 < left ? ex2(fmaf(x[i + 1], kLog2e, -t0)) : 0.f;
+    }
+    sum = sum * ex2(top - t0) + (s0 + s1);
+    top = t;
+    if ((unsigned)y < (unsigned)N) {
+      float zy = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; i++)
+        if (i == y) zy = x[i];
+      zlabel[row] = zy;
+    }
+  }
+
+  __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, bool first,
+                                       bool last, int m, int *status) {
     const int y = row < m ? label[row] - col0 : -1;
     float top = -INFINITY, sum = 0.f;
+    if (CHUNKED) {
+#pragma unroll
+      for (int g = 0; g < 8; g++) {
+        uint32_t r[16];
+        __syncwarp();
+        tmem_ld16(taddr + g * 16, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; i++)
+          z[g][i] = first ? __uint_as_float(r[i]) : z[g][i] + __uint_as_float(r[i]);
+      }
+      if (!last) return;
+#pragma unroll
+      for (int g = 0; g < 8; g++)
+        if (v > col0 + g * 16) group<16>(z[g], v - (col0 + g * 16), y - g * 16, row, top, sum);
+    } else {
 #pragma unroll 1
-    for (int g = 0; g < 4; g++) {
-      uint32_t r[32];
-      __syncwarp();
-      tmem_ld32(taddr + g * 32, r);
-      tmem_wait_ld();
-      const int left = v - (col0 + g * 32);  // columns of this group that exist
-      if (left <= 0) break;
-      if (left < 32) {
+      for (int g = 0; g < 4; g++) {
+        const int left = v - (col0 + g * 32);  // columns of this group that exist
+        if (left <= 0) break;
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld32(taddr + g * 32, r);
+        tmem_wait_ld();
+        float x[32];
 #pragma unroll
-        for (int i = 0; i < 32; i++)
-          if (i >= left) r[i] = 0xFF800000u;  // -inf
-      }
-      float mx = __uint_as_float(r[0]);
-#pragma unroll
-      for (int i = 1; i < 32; i++) mx = fmaxf(mx, __uint_as_float(r[i]));
-      const float t = fmaxf(top, mx * kLog2e);
-      // a row of -inf so far: exponents against 0 (every term is 0)
-      const float t0 = t == -INFINITY ? 0.f : t;
-      float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        s0 += ex2(fmaf(__uint_as_float(r[i]), kLog2e, -t0));
-        s1 += ex2(fmaf(__uint_as_float(r[i + 1]), kLog2e, -t0));
-      }
-      sum = sum * ex2(top - t0) + (s0 + s1);
-      top = t;
-      if ((unsigned)(y - g * 32) < 32u) {
-        float z = 0.f;
-#pragma unroll
-        for (int i = 0; i < 32; i++)
-          if (i == y - g * 32) z = __uint_as_float(r[i]);
-        zlabel[row] = z;
+        for (int i = 0; i < 32; i++) x[i] = __uint_as_float(r[i]);
+        group<32>(x, left, y - g * 32, row, top, sum);
       }
     }
     if (row < m && OS2_DBG_GUARD((col0 >> 7) < parts, status))
@@ -254,7 +278,7 @@ struct GradEpi {
   long pitch;     // multiple of 256
   int v0, v;
 
-  __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, int, int m, int *) {
+  __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, bool, bool, int m, int *) {
     const bool in = row < m;
     const int y = in ? label[row] - v0 - col0 : -1;
     // 2^E p = 2^(z log2 e - lse log2 e + E), so that p's own range does not cut it
@@ -290,32 +314,42 @@ struct GradEpi {
   }
 };
 
-// dH and dW: scaled back, rounded once, to the row that a packed row came from;
-// dH's sums over the pieces stay in FP32 until the last.
+// dW, and dH where it comes out of one product: scaled back, rounded once, to the
+// row that a packed row came from.
+template <bool BF16>
+__device__ __forceinline__ void store32(uint16_t *dst, const float (&x)[32], float s, int left,
+                                        bool vec) {
+  if (left >= 32 && vec) {
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+      reinterpret_cast<uint4 *>(dst)[q] =
+          make_uint4(pack2<BF16>(x[8 * q] * s, x[8 * q + 1] * s),
+                     pack2<BF16>(x[8 * q + 2] * s, x[8 * q + 3] * s),
+                     pack2<BF16>(x[8 * q + 4] * s, x[8 * q + 5] * s),
+                     pack2<BF16>(x[8 * q + 6] * s, x[8 * q + 7] * s));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; i++)
+      if (i < left) dst[i] = pack1<BF16>(x[i] * s);
+  }
+}
+
 template <bool BF16>
 struct StoreEpi {
   uint16_t *out;
   long ld;
   const int *rowmap;    // or null
   const float *scale;
-  float *acc;           // [rows][acc_pitch], acc_pitch a multiple of 256; null with one piece
-  long acc_pitch;
-  int first, last, n;
+  int n;
   bool vec;             // rows of `out` are 16-byte aligned
 
-  __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, int, int m, int *) {
+  __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, bool, bool, int m,
+                                       int *) {
     const bool in = row < m;
     const float s = scale[1];
-    uint16_t *dst = nullptr;
-    if (in && last) dst = out + (size_t)(rowmap ? rowmap[row] : row) * ld + col0;
-    float4 *a = acc && in ? reinterpret_cast<float4 *>(acc + (size_t)row * acc_pitch + col0) : nullptr;
+    uint16_t *dst = in ? out + (size_t)(rowmap ? rowmap[row] : row) * ld + col0 : nullptr;
 #pragma unroll 1
     for (int g = 0; g < 4; g++) {
-      float4 av[8];
-      if (a && !first) {
-#pragma unroll
-        for (int q = 0; q < 8; q++) av[q] = a[g * 8 + q];
-      }
       uint32_t r[32];
       __syncwarp();
       tmem_ld32(taddr + g * 32, r);
@@ -323,60 +357,98 @@ struct StoreEpi {
       float x[32];
 #pragma unroll
       for (int i = 0; i < 32; i++) x[i] = __uint_as_float(r[i]);
-      if (a && !first) {
+      if (in) store32<BF16>(dst + g * 32, x, s, n - (col0 + g * 32), vec);
+    }
+  }
+};
+
+// dH out of several products (pieces of the vocabulary, parts of one): FP32 sums,
+// one array for each part, added to by each piece.
+struct SumEpi {
+  float *acc;           // [splits][rows][pitch], pitch a multiple of 256
+  long rows, pitch;
+  bool add;
+
+  __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int split, bool, bool,
+                                       int m, int *) {
+    const bool in = row < m;
+    float4 *a = reinterpret_cast<float4 *>(acc + ((size_t)split * rows + (in ? row : 0)) * pitch + col0);
+#pragma unroll 1
+    for (int g = 0; g < 4; g++) {
+      float4 av[8];
+      if (add && in) {
+#pragma unroll
+        for (int q = 0; q < 8; q++) av[q] = a[g * 8 + q];
+      }
+      uint32_t r[32];
+      __syncwarp();
+      tmem_ld32(taddr + g * 32, r);
+      tmem_wait_ld();
+      if (in) {
 #pragma unroll
         for (int q = 0; q < 8; q++) {
-          x[4 * q] += av[q].x;
-          x[4 * q + 1] += av[q].y;
-          x[4 * q + 2] += av[q].z;
-          x[4 * q + 3] += av[q].w;
+          float4 x = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                 __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+          if (add) x.x += av[q].x, x.y += av[q].y, x.z += av[q].z, x.w += av[q].w;
+          a[g * 8 + q] = x;
         }
-      }
-      if (!in) continue;
-      if (!last) {
-#pragma unroll
-        for (int q = 0; q < 8; q++)
-          a[g * 8 + q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-        continue;
-      }
-      const int left = n - (col0 + g * 32);
-      if (left >= 32 && vec) {
-#pragma unroll
-        for (int q = 0; q < 4; q++)
-          reinterpret_cast<uint4 *>(dst + g * 32)[q] =
-              make_uint4(pack2<BF16>(x[8 * q] * s, x[8 * q + 1] * s),
-                         pack2<BF16>(x[8 * q + 2] * s, x[8 * q + 3] * s),
-                         pack2<BF16>(x[8 * q + 4] * s, x[8 * q + 5] * s),
-                         pack2<BF16>(x[8 * q + 6] * s, x[8 * q + 7] * s));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; i++)
-          if (i < left) dst[g * 32 + i] = pack1<BF16>(x[i] * s);
       }
     }
   }
 };
 
+// dH from those sums, the parts in their order.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+    k_dh_join(const int *count, const int *rowmap, const float *scale, const float *acc, int splits,
+              long rows, long pitch, int k, uint16_t *out, long ld, bool vec) {
+  next_may_start();
+  wait_for_previous();
+  const float s = scale[1];
+  const long per = pitch / 8, total = per * *count;
+  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
+    const long row = i / per;
+    const int h = (int)(i - row * per) * 8;
+    if (h >= k) continue;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int p = 0; p < splits; p++) {
+      const float4 *a = reinterpret_cast<const float4 *>(acc + ((size_t)p * rows + row) * pitch + h);
+      const float4 u = a[0], v = a[1];
+      x[0] += u.x, x[1] += u.y, x[2] += u.z, x[3] += u.w;
+      x[4] += v.x, x[5] += v.y, x[6] += v.z, x[7] += v.w;
+    }
+    uint16_t *dst = out + (size_t)rowmap[row] * ld + h;
+    if (vec && h + 8 <= k) {
+      *reinterpret_cast<uint4 *>(dst) =
+          make_uint4(pack2<BF16>(x[0] * s, x[1] * s), pack2<BF16>(x[2] * s, x[3] * s),
+                     pack2<BF16>(x[4] * s, x[5] * s), pack2<BF16>(x[6] * s, x[7] * s));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; e++)
+        if (h + e < k) dst[e] = pack1<BF16>(x[e] * s);
+    }
+  }
+}
+
 // ------------------------------------------------------------ joining a row
 __global__ void __launch_bounds__(256)
     k_xent_join(const int *count, const int *rowmap, const float *zlabel, const float2 *part,
                 int parts, float *loss, float *lse) {
+  next_may_start();
+  wait_for_previous();
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= *count) return;
   const float2 *p = part + (size_t)row * parts;
   float top = -INFINITY, sum = 0.f;
   for (int i = lane; i < parts; i += 32) {
     const float2 v = p[i];
-    const float t = fmaxf(top, v.x), t0 = t == -INFINITY ? 0.f : t;
-    sum = sum * ex2(top - t0) + v.y * ex2(v.x - t0);
-    top = t;
+    add_exp(top, sum, v.x, v.y);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     const float x = __shfl_xor_sync(0xffffffffu, top, o), y = __shfl_xor_sync(0xffffffffu, sum, o);
-    const float t = fmaxf(top, x), t0 = t == -INFINITY ? 0.f : t;
-    sum = sum * ex2(top - t0) + y * ex2(x - t0);
-    top = t;
+    add_exp(top, sum, x, y);
   }
   if (lane == 0) {
     const float l = top * kLn2 + logf(sum);
@@ -400,9 +472,30 @@ int piece_columns(long npad, int v) {
   return (int)os2_round_up((size_t)((v + pieces - 1) / pieces), 256);
 }
 
+// Parts of dH's product over a piece of the vocabulary: as many as let all SM
+// pairs work, by an estimate in microseconds (0.55 a stage; the sums written and
+// read once at 5 TB/s).
+int dh_splits(long npad, int k, int vc, int pieces) {
+  const long tiles = npad / 256 * ((k + 255) / 256), pairs = std::max(os2_sm_count() / 2, 1);
+  const int stages = (vc + kStageK - 1) / kStageK;
+  const double bytes = (double)npad * os2_round_up((size_t)k, 256) * 8;
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= std::min(stages, 32); s++) {
+    if (s > 1 && bytes / 2 * s > 268435456.) break;
+    const double t = (double)((tiles * s + pairs - 1) / pairs) * ((stages + s - 1) / s) * 0.55 * pieces +
+                     (s > 1 || pieces > 1 ? bytes * s / 5e6 + 3 : 0);
+    if (t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
 struct Layout {
   long npad, kp;
-  int parts, vc, pieces;
+  int parts, vc, pieces, splits;
   size_t count, rowmap, label, zlabel, part, Hc, Wc, lse_c, grad_c, scale, d, acc, total;
 };
 
@@ -410,7 +503,7 @@ Layout layout(int n, int k, int v, const void *W, int ldw, bool backward) {
   Layout L = {};
   L.npad = (long)os2_round_up((size_t)n, 256);
   L.kp = (long)os2_round_up((size_t)k, 64);
-  L.parts = (v + kBN - 1) / kBN * 2;
+  L.parts = n <= kXentFew ? os2_sm_count() : (v + kBN - 1) / kBN * 2;
   L.vc = piece_columns(std::max(L.npad, 256L), v);
   L.pieces = (v + L.vc - 1) / L.vc;
   size_t at = 0;
@@ -429,7 +522,9 @@ Layout layout(int n, int k, int v, const void *W, int ldw, bool backward) {
     L.grad_c = take((size_t)n * 4);
     L.scale = take(8);
     L.d = take((size_t)L.npad * L.vc * 2);
-    if (L.pieces > 1) L.acc = take((size_t)L.npad * os2_round_up((size_t)k, 256) * 4);
+    L.splits = dh_splits(L.npad, k, std::min(L.vc, v), L.pieces);
+    if (L.pieces * L.splits > 1)
+      L.acc = take((size_t)L.splits * L.npad * os2_round_up((size_t)k, 256) * 4);
   } else {
     L.zlabel = take((size_t)n * 4);
     L.part = take((size_t)n * L.parts * 8);
@@ -456,7 +551,9 @@ cudaError_t prepare(const Layout &L, Prep &p, const uint16_t *&W, long &ldw, voi
   k_xent_prep<<<(p.n + p.rows_cta - 1) / p.rows_cta, kPrepThreads, 0, s>>>(p);
   if (!tma_rows(W, ldw)) {
     uint16_t *wc = at<uint16_t>(ws, L.Wc);
-    k_repack<<<std::min(p.v, 8 * os2_sm_count()), 256, 0, s>>>(W, ldw, wc, L.kp, p.v, p.k);
+    const cudaError_t e = launch_after(k_repack, std::min(p.v, 8 * os2_sm_count()), 256, 0, s, W, ldw,
+                                       wc, L.kp, p.v, p.k);
+    if (e != cudaSuccess) return e;
     W = wc;
     ldw = L.kp;
   }
@@ -468,17 +565,34 @@ cudaError_t forward(Prep p, const uint16_t *W, long ldw, void *ws, const Layout 
                     cudaStream_t s) {
   cudaError_t e = prepare(L, p, W, ldw, ws, s);
   if (e != cudaSuccess) return e;
+  float *zlabel = at<float>(ws, L.zlabel);
+  float2 *part = at<float2>(ws, L.part);
+  if (p.n <= kXentFew) {
+    XentFewArgs a{p.n, p.k, p.v, BF16, p.Hc, L.kp, W, ldw, !L.Wc, p.count, p.label, zlabel, part,
+                  p.status};
+    int parts = 0;
+    e = launch_xent_few(a, &parts, s);
+    if (e != cudaSuccess) return e;
+    return launch_after(k_xent_join, (p.n + 7) / 8, 256, 0, s, p.count, p.rowmap, zlabel, part, parts,
+                        p.loss, p.lse);
+  }
   CUtensorMap mh, mw;
   if (!make_map(&mh, p.Hc, BF16, p.k, p.n, L.kp, false) ||
       !make_map(&mw, W, BF16, p.k, p.v, ldw, false))
     return cudaErrorInvalidValue;
-  const StatsEpi epi{p.label, at<float>(ws, L.zlabel), at<float2>(ws, L.part), L.parts, p.v};
-  const Job job{p.n, p.v, p.k, p.count, nullptr, INT_MAX};
-  e = launch_mm2<BF16, false, false>(mh, mw, job, epi, p.status, s);
+  auto product = [&](auto epi, int chunk) {
+    epi.label = p.label;
+    epi.zlabel = zlabel;
+    epi.part = part;
+    epi.parts = L.parts;
+    epi.v = p.v;
+    return launch_mm2<BF16, false, false>(mh, mw, Job{p.n, p.v, p.k, p.count, nullptr, chunk, 1},
+                                          epi, p.status, s);
+  };
+  e = p.k > 1024 ? product(StatsEpi<true>{}, 1024 / kStageK) : product(StatsEpi<false>{}, INT_MAX);
   if (e != cudaSuccess) return e;
-  k_xent_join<<<(p.n + 7) / 8, 256, 0, s>>>(p.count, p.rowmap, epi.zlabel, epi.part, L.parts,
-                                            p.loss, p.lse);
-  return cudaGetLastError();
+  return launch_after(k_xent_join, (p.n + 7) / 8, 256, 0, s, p.count, p.rowmap, zlabel, part, L.parts,
+                      p.loss, p.lse);
 }
 
 template <bool BF16>
@@ -490,7 +604,7 @@ cudaError_t backward(Prep p, const uint16_t *W, long ldw, uint16_t *dW, long ldd
   cudaError_t e = prepare(L, p, W, ldw, ws, s);
   if (e != cudaSuccess) return e;
   uint16_t *d = at<uint16_t>(ws, L.d);
-  float *acc = L.pieces > 1 ? at<float>(ws, L.acc) : nullptr;
+  float *acc = at<float>(ws, L.acc);
   const long acc_pitch = (long)os2_round_up((size_t)p.k, 256);
   CUtensorMap mh, mht, mw, mwt, md, mdt;
   if (!make_map(&mh, p.Hc, BF16, p.k, p.n, L.kp, false) ||
@@ -505,25 +619,34 @@ cudaError_t backward(Prep p, const uint16_t *W, long ldw, uint16_t *dW, long ldd
         !make_map(&mdt, d, BF16, L.vc, L.npad, L.vc, true))
       return cudaErrorInvalidValue;
     const GradEpi<BF16> ge{p.label, p.lse_c, p.grad_c, p.scale, d, L.vc, v0, vn};
-    e = launch_mm2<BF16, false, false>(mh, mw, Job{p.n, vn, p.k, p.count, nullptr, INT_MAX}, ge,
+    e = launch_mm2<BF16, false, false>(mh, mw, Job{p.n, vn, p.k, p.count, nullptr, INT_MAX, 1}, ge,
                                        p.status, s);
     if (e != cudaSuccess) return e;
     if (p.dH) {
-      const StoreEpi<BF16> se{p.dH, p.lddh, p.rowmap, p.scale, acc, acc_pitch, i == 0,
-                              i == L.pieces - 1, p.k, tma_rows(p.dH, p.lddh)};
-      e = launch_mm2<BF16, false, true>(md, mwt, Job{p.n, p.k, vn, p.count, nullptr, INT_MAX}, se,
-                                        p.status, s);
+      // (a shorter last piece may have fewer stages than parts: those add nothing)
+      const Job job{p.n, p.k, vn, p.count, nullptr, INT_MAX, L.splits};
+      e = L.pieces * L.splits > 1
+              ? launch_mm2<BF16, false, true>(md, mwt, job, SumEpi{acc, L.npad, acc_pitch, i > 0},
+                                              p.status, s)
+              : launch_mm2<BF16, false, true>(
+                    md, mwt, job,
+                    StoreEpi<BF16>{p.dH, p.lddh, p.rowmap, p.scale, p.k, tma_rows(p.dH, p.lddh)},
+                    p.status, s);
       if (e != cudaSuccess) return e;
     }
     if (dW) {
-      const StoreEpi<BF16> se{dW + (size_t)v0 * lddw, lddw, nullptr, p.scale, nullptr, 0, 1, 1,
-                              p.k, tma_rows(dW, lddw)};
-      e = launch_mm2<BF16, true, true>(mdt, mht, Job{vn, p.k, p.n, nullptr, p.count, INT_MAX}, se,
+      const StoreEpi<BF16> se{dW + (size_t)v0 * lddw, lddw, nullptr, p.scale, p.k,
+                              tma_rows(dW, lddw)};
+      e = launch_mm2<BF16, true, true>(mdt, mht, Job{vn, p.k, p.n, nullptr, p.count, INT_MAX, 1}, se,
                                        p.status, s);
       if (e != cudaSuccess) return e;
     }
   }
-  return cudaSuccess;
+  if (!p.dH || L.pieces * L.splits == 1) return cudaSuccess;
+  const long groups = acc_pitch / 8 * p.n;
+  return launch_after(k_dh_join<BF16>, (int)std::min<long>((groups + 255) / 256, 16L * os2_sm_count()),
+                      256, 0, s, p.count, p.rowmap, p.scale, acc, L.splits, L.npad, acc_pitch, p.k,
+                      p.dH, p.lddh, tma_rows(p.dH, p.lddh));
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -14,10 +14,11 @@
 // TMA in the 128-byte swizzle, and no transposed copy is made.  Entries outside
 // a tensor map read as zero.
 //
-// Warps (320 threads): 0 TMA producer, 1 MMA issuer, 2-9 epilogue (each TMEM
-// lane quarter twice: columns 0-127 and 128-255).  Two epilogue warps a
-// quarter, because the epilogues here do arithmetic on every entry (an
-// exponential, an integer sum kept in 128 registers a thread).
+// Warps (384 threads): 0 TMA producer, 1 MMA issuer, 4-11 epilogue (each TMEM
+// lane quarter twice: columns 0-127 and 128-255; 2 and 3 fill the first
+// warpgroup).  Two epilogue warps a quarter, because the epilogues here do
+// arithmetic on every entry, and most of the registers: one of them keeps 128
+// sums a thread.
 // Every wait is bounded; on expiry the CTA records OS2_ERR_TIMEOUT, lets its
 // copies and MMAs drain (again bounded), frees its TMEM and returns.
 #pragma once
@@ -44,7 +45,10 @@ constexpr int kStages = 3;
 constexpr uint32_t kBlockBytes = kHalf * kBK * 2;              // one operand, one k-block
 constexpr uint32_t kOpBytes = kKbStage * kBlockBytes;          // one operand, one stage
 constexpr int kEpiThreads = 256;
-constexpr int kThreads = 64 + kEpiThreads;
+constexpr int kThreads = 128 + kEpiThreads;
+// registers a thread: 384 x 168 at launch >= 128 x 64 + 256 x 216
+constexpr int kRegsMisc = 64, kRegsEpi = 216;
+static_assert(128 * kRegsMisc + 256 * kRegsEpi <= kThreads * 168, "registers");
 constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kOpBytes + 256;
 static_assert(kSmem <= 227 * 1024, "shared memory of the product kernel");
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (about 2 s)
@@ -55,6 +59,7 @@ struct Job {
   const int *m_dev;   // if set, the rows that count (<= m), known on the device only
   const int *k_dev;   // if set, the terms that count (<= k); the rest of the last stage is zero
   int chunk;          // stages per accumulation chunk (INT_MAX: the whole of k)
+  int splits;         // parts of k, each a job of its own (at most the stages of k; 1 with k_dev)
 };
 
 __device__ __forceinline__ void set_status(int *status, int code) {
@@ -72,12 +77,13 @@ __device__ __forceinline__ void tile_coords(int t, int tiles_m, int tiles_n, int
 }
 
 // Epi: a copyable struct with
-//   void unit(uint32_t taddr, int row, int col0, int chunk, int nchunks, int m, int *status)
+//   void unit(uint32_t taddr, int row, int col0, int split, bool first, bool last, int m,
+//             int *status)
 // called by every lane of an epilogue warp (converged) with the TMEM address of
 // its lane quarter's 128 columns, its own row of the output and the first of
 // its 128 columns.  It reads TMEM with tcgen05.ld and waits for the loads; rows
 // from m on and columns past the output are its business.  It may keep state
-// between the chunks of a tile (chunk == nchunks - 1 ends one).
+// between the chunks of a job (first, last).
 template <bool BF16, bool A_MN, bool B_MN, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_mm2(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
@@ -102,16 +108,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int pair = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
-
-  // counts known on the device only, never above the host's
-  const int m = job.m_dev ? min(max(*job.m_dev, 0), job.m) : job.m;
-  const int k = job.k_dev ? min(max(*job.k_dev, 0), job.k) : job.k;
-  const int tiles_m = (m + 2 * kHalf - 1) / (2 * kHalf), tiles_n = (job.n + kBN - 1) / kBN;
-  const int njobs = tiles_m * tiles_n;
-  // no term at all still runs one stage, of zeros, so that the epilogue writes its rows
-  const int stages_k = max((k + kStageK - 1) / kStageK, 1);
-  const int nchunks = (stages_k - 1) / job.chunk + 1;
-  const int k_first = k == 0 ? (job.k + 255) / 256 * 256 : 0;  // past every map: zeros
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; s++) {
@@ -140,117 +136,137 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, used = 0, last_par = 0;
-      bool ok = true;
-      for (int t = pair; ok && t < njobs; t += npairs) {
-        int tm, tn;
-        tile_coords(t, tiles_m, tiles_n, tm, tn);
-        const int ra = tm * 2 * kHalf + (int)rank * kHalf, rb = tn * kBN + (int)rank * kHalf;
-        for (int ks = 0; ks < stages_k; ks++) {
-          if (!mbar_wait_cluster_bounded(&empty[stage], phase ^ 1, s_abort, kWaitLimit)) {
-            *s_abort = 1;
-            set_status(status, OS2_ERR_TIMEOUT);
-            ok = false;
-            break;
-          }
-          const uint32_t fbar = mapa_shared(smem_u32(&full[stage]), 0);
-          if (leader) mbar_arrive_expect_tx(&full[stage], 4 * kOpBytes);
-#pragma unroll
-          for (int h = 0; h < kKbStage; h++) {
-            const int kx = k_first + ks * kStageK + h * kBK;
-            uint8_t *da = sA + stage * kOpBytes + h * kBlockBytes;
-            uint8_t *db = sB + stage * kOpBytes + h * kBlockBytes;
-            if (A_MN) {  // two boxes of 64 rows of the tile x 64 terms
-              tma_load_3d_pair(da, &mapA, fbar, ra, kx, 0);
-              tma_load_3d_pair(da + kBlockBytes / 2, &mapA, fbar, ra + 64, kx, 0);
-            } else {
-              tma_load_3d_pair(da, &mapA, fbar, kx, ra, 0);
-            }
-            if (B_MN) {
-              tma_load_3d_pair(db, &mapB, fbar, rb, kx, 0);
-              tma_load_3d_pair(db + kBlockBytes / 2, &mapB, fbar, rb + 64, kx, 0);
-            } else {
-              tma_load_3d_pair(db, &mapB, fbar, kx, rb, 0);
-            }
-          }
-          used |= 1u << stage;
-          last_par = (last_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
-      }
-      // the pair's copies complete on the leader's barriers: it waits for the last of each stage
-      if (leader)
-        for (int s = 0; s < kStages; s++)
-          if (used >> s & 1) {
-            volatile int no_abort = 0;
-            mbar_wait_cluster_bounded(&full[s], (last_par >> s) & 1, &no_abort, kWaitLimit);
-          }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (leader && lane == 0) {
-      int stage = 0, unit = 0;
-      uint32_t phase = 0;
-      uint32_t aphase[2] = {0, 0};
-      bool ok = true;
-      for (int t = pair; ok && t < njobs; t += npairs) {
-        for (int c = 0; ok && c < nchunks; c++, unit++) {
-          const int buf = unit & 1;
-          if (!mbar_wait_cluster_bounded(&acc_empty[buf], aphase[buf] ^ 1, s_abort, kWaitLimit)) {
-            *s_abort = 1;
-            set_status(status, OS2_ERR_TIMEOUT);
-            ok = false;
-            break;
-          }
-          aphase[buf] ^= 1;
-          tc_fence_after();
-          const uint32_t d = tmem_base + (uint32_t)(buf * kBN);
-          const int ks0 = c * job.chunk, ks1 = c == nchunks - 1 ? stages_k : ks0 + job.chunk;
-          for (int ks = ks0; ks < ks1; ks++) {
-            if (!mbar_wait_cluster_bounded(&full[stage], phase, s_abort, kWaitLimit)) {
+  next_may_start();
+  wait_for_previous();
+  // counts known on the device only, never above the host's
+  const int m = job.m_dev ? min(max(*job.m_dev, 0), job.m) : job.m;
+  const int k = job.k_dev ? min(max(*job.k_dev, 0), job.k) : job.k;
+  const int tiles_m = (m + 2 * kHalf - 1) / (2 * kHalf), tiles_n = (job.n + kBN - 1) / kBN;
+  const int tiles = tiles_m * tiles_n, njobs = tiles * job.splits;
+  // no term at all still runs one stage, of zeros, so that the epilogue writes its rows
+  const int stages_k = max((k + kStageK - 1) / kStageK, 1);
+  // job t: split t / tiles of tile t % tiles, over stages [stage0(t), stage1(t))
+  auto stage0 = [&](int t) { return t / tiles * stages_k / job.splits; };
+  auto stage1 = [&](int t) { return (t / tiles + 1) * stages_k / job.splits; };
+  const int k_first = k == 0 ? (job.k + 255) / 256 * 256 : 0;  // past every map: zeros
+
+  if (warp < 4) {
+    regs_fewer<kRegsMisc>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      if (lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0, used = 0, last_par = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < njobs; t += npairs) {
+          int tm, tn;
+          tile_coords(t % tiles, tiles_m, tiles_n, tm, tn);
+          const int ra = tm * 2 * kHalf + (int)rank * kHalf, rb = tn * kBN + (int)rank * kHalf;
+          for (int ks = stage0(t); ks < stage1(t); ks++) {
+            if (!mbar_wait_bounded(&empty[stage], phase ^ 1, s_abort, kWaitLimit)) {
               *s_abort = 1;
               set_status(status, OS2_ERR_TIMEOUT);
               ok = false;
               break;
             }
-            tc_fence_after();
+            const uint32_t fbar = mapa_shared(smem_u32(&full[stage]), 0);
+            if (leader) mbar_arrive_expect_tx(&full[stage], 4 * kOpBytes);
 #pragma unroll
             for (int h = 0; h < kKbStage; h++) {
-              const uint32_t a = smem_u32(sA + stage * kOpBytes + h * kBlockBytes);
-              const uint32_t b = smem_u32(sB + stage * kOpBytes + h * kBlockBytes);
-              // MN-major: 8-term atoms 1024 bytes apart, 64-row blocks 8192
-              const uint64_t ad = A_MN ? sdesc_mn128(a, kBlockBytes / 2, 1024) : sdesc_k128(a);
-              const uint64_t bd = B_MN ? sdesc_mn128(b, kBlockBytes / 2, 1024) : sdesc_k128(b);
-              constexpr uint64_t AS = (A_MN ? 16 * 128 : 32) >> 4, BS = (B_MN ? 16 * 128 : 32) >> 4;
-#pragma unroll
-              for (int kk = 0; kk < kBK / 16; kk++)
-                umma2_f16(d, ad + AS * kk, bd + BS * kk, IDESC,
-                          (ks > ks0 || h > 0 || kk > 0) ? 1u : 0u);
+              const int kx = k_first + ks * kStageK + h * kBK;
+              uint8_t *da = sA + stage * kOpBytes + h * kBlockBytes;
+              uint8_t *db = sB + stage * kOpBytes + h * kBlockBytes;
+              if (A_MN) {  // two boxes of 64 rows of the tile x 64 terms
+                tma_load_3d_pair(da, &mapA, fbar, ra, kx, 0);
+                tma_load_3d_pair(da + kBlockBytes / 2, &mapA, fbar, ra + 64, kx, 0);
+              } else {
+                tma_load_3d_pair(da, &mapA, fbar, kx, ra, 0);
+              }
+              if (B_MN) {
+                tma_load_3d_pair(db, &mapB, fbar, rb, kx, 0);
+                tma_load_3d_pair(db + kBlockBytes / 2, &mapB, fbar, rb + 64, kx, 0);
+              } else {
+                tma_load_3d_pair(db, &mapB, fbar, kx, rb, 0);
+              }
             }
-            umma2_commit_mc(&empty[stage], 0x3);
+            used |= 1u << stage;
+            last_par = (last_par & ~(1u << stage)) | (phase << stage);
             if (++stage == kStages) {
               stage = 0;
               phase ^= 1;
             }
           }
-          if (ok) umma2_commit_mc(&acc_full[buf], 0x3);
         }
+        // the pair's copies complete on the leader's barriers: it waits for the last of each stage
+        if (leader)
+          for (int s = 0; s < kStages; s++)
+            if (used >> s & 1) {
+              volatile int no_abort = 0;
+              mbar_wait_bounded(&full[s], (last_par >> s) & 1, &no_abort, kWaitLimit);
+            }
       }
-      umma2_commit_mc(mma_done, 0x1);
-      volatile int no_abort = 0;
-      mbar_wait_bounded(mma_done, 0, &no_abort, kWaitLimit);
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      if (leader && lane == 0) {
+        int stage = 0, unit = 0;
+        uint32_t phase = 0;
+        uint32_t aphase[2] = {0, 0};
+        bool ok = true;
+        for (int t = pair; ok && t < njobs; t += npairs) {
+          const int begin = stage0(t), end = stage1(t);
+          for (int ks0 = begin; ok && ks0 < end; unit++) {
+            const int buf = unit & 1;
+            if (!mbar_wait_bounded(&acc_empty[buf], aphase[buf] ^ 1, s_abort, kWaitLimit)) {
+              *s_abort = 1;
+              set_status(status, OS2_ERR_TIMEOUT);
+              ok = false;
+              break;
+            }
+            aphase[buf] ^= 1;
+            tc_fence_after();
+            const uint32_t d = tmem_base + (uint32_t)(buf * kBN);
+            const int ks1 = end - ks0 > job.chunk ? ks0 + job.chunk : end;
+            for (int ks = ks0; ks < ks1; ks++) {
+              if (!mbar_wait_bounded(&full[stage], phase, s_abort, kWaitLimit)) {
+                *s_abort = 1;
+                set_status(status, OS2_ERR_TIMEOUT);
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll
+              for (int h = 0; h < kKbStage; h++) {
+                const uint32_t a = smem_u32(sA + stage * kOpBytes + h * kBlockBytes);
+                const uint32_t b = smem_u32(sB + stage * kOpBytes + h * kBlockBytes);
+                // MN-major: 8-term atoms 1024 bytes apart, 64-row blocks 8192
+                const uint64_t ad = A_MN ? sdesc_mn128(a, kBlockBytes / 2, 1024) : sdesc_k128(a);
+                const uint64_t bd = B_MN ? sdesc_mn128(b, kBlockBytes / 2, 1024) : sdesc_k128(b);
+                constexpr uint64_t AS = (A_MN ? 16 * 128 : 32) >> 4, BS = (B_MN ? 16 * 128 : 32) >> 4;
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; kk++)
+                  umma2_f16(d, ad + AS * kk, bd + BS * kk, IDESC,
+                            (ks > ks0 || h > 0 || kk > 0) ? 1u : 0u);
+              }
+              umma2_commit_mc(&empty[stage], 0x3);
+              if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+              }
+            }
+            if (ok) umma2_commit_mc(&acc_full[buf], 0x3);
+            ks0 = ks1;
+          }
+        }
+        umma2_commit_mc(mma_done, 0x1);
+        volatile int no_abort = 0;
+        mbar_wait_bounded(mma_done, 0, &no_abort, kWaitLimit);
+      }
     }
   } else {
+    regs_more<kRegsEpi>();
     // ------------------------------------------------------------ epilogue
     Epi epi = epi_in;
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * 128;
     const uint32_t empty_leader[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0),
                                       mapa_shared(smem_u32(&acc_empty[1]), 0)};
@@ -259,13 +275,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int t = pair; ok && t < njobs; t += npairs) {
       int tm, tn;
-      tile_coords(t, tiles_m, tiles_n, tm, tn);
+      tile_coords(t % tiles, tiles_m, tiles_n, tm, tn);
       const int row = tm * 2 * kHalf + (int)rank * kHalf + quarter * 32 + lane;
       const int col0 = tn * kBN + half * 128;
-      for (int c = 0; c < nchunks; c++, unit++) {
+      const int begin = stage0(t), end = stage1(t);
+      for (int ks0 = begin; ks0 < end; unit++) {
+        const int ks1 = end - ks0 > job.chunk ? ks0 + job.chunk : end;
         const int buf = unit & 1;
         // every lane waits (acquire), then the warp reconverges on one verdict
-        ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(&acc_full[buf], aphase[buf],
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[buf], aphase[buf],
                                                                s_abort, kWaitLimit));
         if (!ok) {
           *s_abort = 1;
@@ -274,9 +292,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         aphase[buf] ^= 1;
         tc_fence_after();
-        epi.unit(lane_base + (uint32_t)(buf * kBN), row, col0, c, nchunks, m, status);
+        epi.unit(lane_base + (uint32_t)(buf * kBN), row, col0, t / tiles, ks0 == begin, ks1 == end,
+                 m, status);
         tc_fence_before();
-        mbar_arrive_cluster(empty_leader[buf]);
+        mbar_arrive_remote(empty_leader[buf]);
+        ks0 = ks1;
       }
     }
   }
@@ -323,6 +343,23 @@ inline bool make_map(CUtensorMap *map, const void *base, bool bf16, long cols, l
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Launches a kernel that waits (wait_for_previous) for the one in front of it.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), int grid, int block, size_t smem, cudaStream_t s,
+                         const A &...args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 template <bool BF16, bool A_MN, bool B_MN, class Epi>
 cudaError_t launch_mm2(const CUtensorMap &ma, const CUtensorMap &mb, const Job &job,
                        const Epi &epi, int *status, cudaStream_t s) {
@@ -333,11 +370,12 @@ cudaError_t launch_mm2(const CUtensorMap &ma, const CUtensorMap &mb, const Job &
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   });
   if (attr_err != cudaSuccess) return attr_err;
-  const long tiles = (long)((job.m + 2 * kHalf - 1) / (2 * kHalf)) * ((job.n + kBN - 1) / kBN);
-  if (tiles <= 0) return cudaSuccess;
-  const int pairs = (int)std::min<long>(std::max(os2_sm_count() / 2, 1), tiles);
-  k_mm2<BF16, A_MN, B_MN, Epi><<<2 * pairs, kThreads, kSmem, s>>>(ma, mb, job, epi, status);
-  return cudaGetLastError();
+  const long jobs = (long)((job.m + 2 * kHalf - 1) / (2 * kHalf)) * ((job.n + kBN - 1) / kBN) *
+                    job.splits;
+  if (jobs <= 0) return cudaSuccess;
+  const int pairs = (int)std::min<long>(std::max(os2_sm_count() / 2, 1), jobs);
+  return launch_after(k_mm2<BF16, A_MN, B_MN, Epi>, 2 * pairs, kThreads, kSmem, s, ma, mb, job, epi,
+                      status);
 }
 
 }  // namespace os2mm

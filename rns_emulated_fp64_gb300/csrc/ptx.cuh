@@ -73,6 +73,16 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// Kernels of one call overlap their starts: each lets the next one begin, and
+// touches nothing that an earlier one reads or writes before it has waited for
+// the end of the one in front (which has itself waited for its own).
+__device__ __forceinline__ void next_may_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Moves registers between the warpgroups of a block (all warps of a warpgroup
 // execute it; the sum over the warpgroups must not pass what the block was
 // launched with).

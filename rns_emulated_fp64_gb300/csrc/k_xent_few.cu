@@ -303,9 +303,7 @@ cudaError_t launch(const XentFewArgs &a, int *parts, cudaStream_t s) {
 
 template <bool BF16>
 cudaError_t launch_t(const XentFewArgs &a, int *parts, cudaStream_t s) {
-  return a.n <= 8    ? launch<BF16, 1>(a, parts, s)
-         : a.n <= 16 ? launch<BF16, 2>(a, parts, s)
-                     : launch<BF16, 4>(a, parts, s);
+  return a.n <= 8 ? launch<BF16, 1>(a, parts, s) : launch<BF16, 2>(a, parts, s);
 }
 
 }  // namespace

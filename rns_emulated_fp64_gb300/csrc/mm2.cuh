@@ -49,7 +49,8 @@ constexpr int kThreads = 128 + kEpiThreads;
 // registers a thread: 384 x 168 at launch >= 128 x 64 + 256 x 216
 constexpr int kRegsMisc = 64, kRegsEpi = 216;
 static_assert(128 * kRegsMisc + 256 * kRegsEpi <= kThreads * 168, "registers");
-constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kOpBytes + 256;
+constexpr uint32_t kScratch = 32 * 80;          // an epilogue warp's own shared memory
+constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kOpBytes + 256 + kEpiThreads / 32 * kScratch;
 static_assert(kSmem <= 227 * 1024, "shared memory of the product kernel");
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (about 2 s)
 
@@ -78,12 +79,13 @@ __device__ __forceinline__ void tile_coords(int t, int tiles_m, int tiles_n, int
 
 // Epi: a copyable struct with
 //   void unit(uint32_t taddr, int row, int col0, int split, bool first, bool last, int m,
-//             int *status)
+//             uint8_t *scratch, int *status)
 // called by every lane of an epilogue warp (converged) with the TMEM address of
 // its lane quarter's 128 columns, its own row of the output and the first of
 // its 128 columns.  It reads TMEM with tcgen05.ld and waits for the loads; rows
 // from m on and columns past the output are its business.  It may keep state
-// between the chunks of a job (first, last).
+// between the chunks of a job (first, last).  scratch: kScratch bytes of the
+// warp's own.
 template <bool BF16, bool A_MN, bool B_MN, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_mm2(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
@@ -270,6 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * 128;
     const uint32_t empty_leader[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0),
                                       mapa_shared(smem_u32(&acc_empty[1]), 0)};
+    uint8_t *scratch = reinterpret_cast<uint8_t *>(full) + 256 + (warp - 4) * kScratch;
     uint32_t aphase[2] = {0, 0};
     int unit = 0;
     bool ok = true;
@@ -293,7 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         aphase[buf] ^= 1;
         tc_fence_after();
         epi.unit(lane_base + (uint32_t)(buf * kBN), row, col0, t / tiles, ks0 == begin, ks1 == end,
-                 m, status);
+                 m, scratch, status);
         tc_fence_before();
         mbar_arrive_remote(empty_leader[buf]);
         ks0 = ks1;

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as ct
+import operator
 
 import torch
 
@@ -240,22 +241,25 @@ class XentFunction(torch.autograd.Function):
 
 
 # -------------------------------------------------------------------- AdamW
+_dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape")
+
+
 def _pointers(ts):
-    return (ct.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
+    return (ct.c_void_p * len(ts))(*map(torch.Tensor.data_ptr, ts))
 
 
 def _list(ts, name, shapes, index, dtypes):
     """Checks a list of tensors, one for each parameter; returns their type."""
     if len(ts) != len(shapes):
         raise ValueError(f"{name}: {len(ts)} tensors for {len(shapes)} parameters")
-    dtype = ts[0].dtype
-    if dtype not in dtypes:
-        raise ValueError(f"{name} must be " + " or ".join(str(t) for t in dtypes))
-    for t, shape in zip(ts, shapes):
-        if (t.shape != shape or t.dtype is not dtype or t.get_device() != index or
-                not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous, of one type, on one CUDA device, and "
-                             "match the parameters")
+    types = set(map(_dtype_of, ts))
+    dtype = types.pop()
+    if types or dtype not in dtypes:
+        raise ValueError(f"{name} must be all " + " or all ".join(str(t) for t in dtypes))
+    if (list(map(_shape_of, ts)) != shapes or set(map(torch.Tensor.get_device, ts)) != {index} or
+            not all(map(torch.Tensor.is_contiguous, ts))):
+        raise ValueError(f"{name} must be contiguous, on one CUDA device, and of the parameters' "
+                         "shapes")
     return dtype
 
 
@@ -273,23 +277,24 @@ def adamw(params, grads, exp_avg, exp_avg_sq, *, step: int, lr: float, beta1: fl
     index = params[0].get_device()
     if index < 0:
         raise ValueError("params must be on one CUDA device")
-    shapes = [p.shape for p in params]
+    shapes = list(map(_shape_of, params))
     pt = _list(params, "params", shapes, index, _DTYPE)
     gt = _list(grads, "grads", shapes, index, _DTYPE)
     q8 = exp_avg_scales is not None or exp_avg_sq_scales is not None
     _list(exp_avg, "exp_avg", shapes, index, _INT8 if q8 else (torch.float32,))
     _list(exp_avg_sq, "exp_avg_sq", shapes, index, (torch.uint8,) if q8 else (torch.float32,))
-    sizes = [p.numel() for p in params]
+    sizes = list(map(torch.Tensor.numel, params))
     scales = (None, None)
     if q8:
         for ss, name in ((exp_avg_scales, "exp_avg_scales"), (exp_avg_sq_scales, "exp_avg_sq_scales")):
             if ss is None or len(ss) != len(params):
                 raise ValueError(f"{name}: one tensor for each parameter")
-            for s, n in zip(ss, sizes):
-                if (s.dtype is not torch.float32 or s.get_device() != index or
-                        not s.is_contiguous() or s.numel() != -(-n // ADAMW_BLOCK)):
-                    raise ValueError(f"{name} must be contiguous float32, one value for each "
-                                     f"{ADAMW_BLOCK} elements")
+            if (set(map(_dtype_of, ss)) != {torch.float32} or
+                    set(map(torch.Tensor.get_device, ss)) != {index} or
+                    not all(map(torch.Tensor.is_contiguous, ss)) or
+                    list(map(torch.Tensor.numel, ss)) != [-(-n // ADAMW_BLOCK) for n in sizes]):
+                raise ValueError(f"{name} must be contiguous float32, one value for each "
+                                 f"{ADAMW_BLOCK} elements")
         scales = _pointers(exp_avg_scales), _pointers(exp_avg_sq_scales)
     with _on(index, stream):
         _check(load().os2_adamw(len(params), (ct.c_longlong * len(params))(*sizes),

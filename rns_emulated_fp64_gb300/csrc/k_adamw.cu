@@ -191,7 +191,8 @@ __device__ __forceinline__ void codes(const Encode &e, float m, float v, uint32_
   const float x = sqrt_fast(fabsf(m) * e.rm) * 127.0f;
   const float y = sqrt_fast(sqrt_fast(v * e.rv)) * 255.0f;
   float p = x + kRound, q = y + kRound;
-  // NaN too; in a block of Inf or NaN the exact way gives what the division gives
+  // NaN too (a block that holds Inf or NaN has such a scale: whatever its codes, its
+  // values are not numbers)
   if (!(fabsf(x - (p - kRound)) <= e.dm) || !(fabsf(y - (q - kRound)) <= e.dv)) {
     if (e.am > 0.f) p = rintf(__fmul_rn(__fsqrt_rn(__fdiv_rn(fabsf(m), e.am)), 127.0f)) + kRound;
     if (e.av > 0.f)
@@ -202,9 +203,10 @@ __device__ __forceinline__ void codes(const Encode &e, float m, float v, uint32_
   cv = max(__float_as_uint(q), 0x4B400000u + (v > 0.f ? 1u : 0u));
 }
 
-// The largest of a warp's non-negative values (whose bits order as they do).
-__device__ __forceinline__ float warp_max(float x) {
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+// The largest magnitude by its bits, which order as the values do and put Inf and
+// NaN above every number.
+__device__ __forceinline__ void larger(uint32_t &top, float x) {
+  top = max(top, __float_as_uint(x) & 0x7FFFFFFFu);
 }
 
 template <int PT, int GT, bool Q8>
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, Q8 ? 6 : 1) k_adamw(const __grid_con
     m_values(cm.w[0], cm.w[1], ts.ms[lo][block], m);
     v_values(cv.w[0], cv.w[1], ts.vs[lo][block], v);
   }
-  float am = 0.f, av = 0.f;  // the block's largest magnitudes
+  uint32_t am = 0, av = 0;  // the block's largest magnitudes
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     const float g = Elem<GT>::get(g8[i]);
@@ -256,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, Q8 ? 6 : 1) k_adamw(const __grid_con
     const float d = sqrt_fast(v[i] * st.c2) + st.eps;  // 2^-22 of the update
     p8[i] = Elem<PT>::put(Elem<PT>::get(p8[i]) * st.decay - __fdividef(m[i] * st.lr_c1, d));
     if (Q8) {
-      am = fmaxf(am, fabsf(m[i]));
-      av = fmaxf(av, v[i]);
+      larger(am, m[i]);
+      larger(av, v[i]);
     }
   }
   store8(pp, p8, n, vec);
@@ -265,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, Q8 ? 6 : 1) k_adamw(const __grid_con
     store8(static_cast<float *>(ts.m[lo]) + at, m, n, vec);
     store8(static_cast<float *>(ts.v[lo]) + at, v, n, vec);
   } else {
-    const Encode e = encode_with(warp_max(am), warp_max(av));
+    const Encode e = encode_with(__uint_as_float(__reduce_max_sync(0xffffffffu, am)),
+                                 __uint_as_float(__reduce_max_sync(0xffffffffu, av)));
     union {
       uint8_t b[8];
       uint32_t w[2];

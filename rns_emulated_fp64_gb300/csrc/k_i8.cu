@@ -13,6 +13,8 @@
 
 #include "i8.cuh"
 
+using namespace os2mm;
+
 namespace {
 
 template <int DT>
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(kQThreads)
             bool vecq, unsigned *zero, int nzero) {
   __shared__ uint32_t s_top[kQThreads / 32];
   const int row = blockIdx.x, tid = threadIdx.x;
-  asm volatile("griddepcontrol.launch_dependents;");
+  next_may_start();
   if (row == 0)
     for (int i = tid; i < nzero; i += kQThreads) zero[i] = 0;
   const char *x = static_cast<const char *>(X) + (size_t)row * ldx * (DT == OS2_F32 ? 4 : 2);
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kQThreads)
 __global__ void __launch_bounds__(kQThreads)
     k_widen_tokens(int k, const int8_t *A, long lda, __half *dst, long pitch, bool vec,
                    unsigned *zero, int nzero) {
-  asm volatile("griddepcontrol.launch_dependents;");
+  next_may_start();
   const int row = blockIdx.x, tid = threadIdx.x;
   if (row == 0)
     for (int i = tid; i < nzero; i += kQThreads) zero[i] = 0;
@@ -157,6 +159,7 @@ __global__ void __launch_bounds__(kQThreads)
 // for such B): 16 bytes a thread, read as words that straddle them.
 __global__ void __launch_bounds__(256)
     k_align_rows(int n, int k, const int8_t *B, long ldb, int8_t *dst, long pitch) {
+  next_may_start();  // (beside the kernel that quantises the tokens: they share nothing)
   const long per = pitch / 16, total = per * n;
   for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
     const long r = i / per;
@@ -180,6 +183,7 @@ __global__ void __launch_bounds__(256)
     }
     *reinterpret_cast<uint4 *>(dst + r * pitch + h) = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  wait_for_previous();  // the next kernel's wait for this one is one for that one too
 }
 
 // Without terms, the bias.
@@ -255,8 +259,10 @@ cudaError_t product(int m, int n, int k, const Layout &L, char *ws, const float 
   if (L.wpitch) {
     int8_t *w = reinterpret_cast<int8_t *>(ws + L.weights);
     const long pieces = L.wpitch / 16 * n;
-    k_align_rows<<<(unsigned)std::min<long>((pieces + 255) / 256, 16L * os2_sm_count()), 256, 0, s>>>(
-        n, k, B, ldb, w, L.wpitch);
+    const cudaError_t e =
+        launch_after(k_align_rows, (int)std::min<long>((pieces + 255) / 256, 16L * os2_sm_count()),
+                     256, 0, s, n, k, B, ldb, w, L.wpitch);
+    if (e != cudaSuccess) return e;
     B = w;
     ldb = L.wpitch;
   }
@@ -288,7 +294,8 @@ os2_status check(int m, int n, int k, const void *A, int lda, const void *B, int
   if (m > 0 && n > 0 && (!C || !aligned(C, elem_size(ot)) || !sb || !aligned(sb, 4) ||
                          (bias && !aligned(bias, 4)) || (k > 0 && (!A || !B))))
     return OS2_ERR_INVALID_ARG;
-  if (k > kMaxK || m > kMaxDim || n > kMaxDim) return OS2_ERR_UNSUPPORTED;
+  if (k > kMaxK || m > kMaxDim || n > kMaxDim || (long long)m * n > (1LL << 40))
+    return OS2_ERR_UNSUPPORTED;
   return OS2_OK;
 }
 
@@ -298,6 +305,7 @@ extern "C" os2_status os2_quantize_rows(int m, int k, int dtype, const void *X, 
                                         int ldq, float *scale, void *stream) {
   if (m < 0 || k < 0 || ldx < k || ldq < k || !is_dtype(dtype)) return OS2_ERR_INVALID_ARG;
   if (m == 0) return OS2_OK;
+  if (k > (1 << 30)) return OS2_ERR_UNSUPPORTED;
   if (!scale || !aligned(scale, 4) || (k > 0 && (!X || !q || !aligned(X, elem_size(dtype)))))
     return OS2_ERR_INVALID_ARG;
   return quantize(m, k, dtype, X, ldx, q, ldq, scale, static_cast<cudaStream_t>(stream)) ==
@@ -307,7 +315,9 @@ extern "C" os2_status os2_quantize_rows(int m, int k, int dtype, const void *X, 
 }
 
 extern "C" size_t os2_i8gemm_workspace_size(int m, int n, int k, const void *B, int ldb) {
-  if (m < 0 || n < 0 || k < 0 || k > kMaxK || m > kMaxDim || n > kMaxDim || ldb < k) return 0;
+  if (m < 0 || n < 0 || k < 0 || k > kMaxK || m > kMaxDim || n > kMaxDim || ldb < k ||
+      (long long)m * n > (1LL << 40))
+    return 0;
   return layout(m, n, k, B, ldb).total;
 }
 

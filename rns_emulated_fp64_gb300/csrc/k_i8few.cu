@@ -22,8 +22,6 @@
 // for the one in front of it on the stream, which quantises the tokens: they are
 // inputs of the call, and nothing in front of that kernel can be writing them
 // still.  Every wait is bounded, as in mm2.cuh.
-#include <map>
-
 #include "i8.cuh"
 
 using namespace os2i8;
@@ -262,7 +260,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; e++) {
             const int c = ch + 8 * (e >> 1), to = q * 8 + 2 * t4 + (e & 1);
-            if (c < j.n && to < j.m)
+            if (c < j.n && to < j.m && OS2_DBG_GUARD(c >= 0 && j.ldy >= j.n, status))
               store_y(j.y, j.out_dtype, (size_t)to * j.ldy + c,
                       (float)sum[q][e] * j.sa[to] * sb[e >> 1] + bias[e >> 1]);
           }
@@ -319,12 +317,19 @@ cudaError_t launch_i8few(const I8Args &a, cudaStream_t s) {
 // ------------------------------------------------------------- cluster sizes
 namespace {
 
-// Clusters of c CTAs of a kernel that run at once on the device.
+// Clusters of c CTAs of a kernel that run at once on the device (asked once for
+// each kernel; a handful of kernels).
 int resident_clusters(const void *kernel, int threads, size_t smem, int c) {
   static std::mutex mu;
-  static std::map<std::pair<const void *, int>, int> known;
+  static struct {
+    const void *kernel;
+    int n[9];
+  } known[16] = {};
   std::lock_guard<std::mutex> g(mu);
-  int &n = known[{kernel, c}];
+  int i = 0;
+  while (i < 15 && known[i].kernel && known[i].kernel != kernel) i++;
+  if (known[i].kernel != kernel) known[i] = {kernel, {}};
+  int &n = known[i].n[c];
   if (!n) {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;

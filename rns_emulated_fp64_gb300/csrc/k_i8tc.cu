@@ -124,6 +124,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Threads<NT>::all, 1)
   cluster_sync();  // the peer's barriers are initialised before any remote arrive / copy
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
+  next_may_start();
+  wait_for_previous();  // the tokens, their scales, the counters, copied weights
 
   auto gave_up = [&]() {
     *s_abort = 1;
@@ -342,6 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Threads<NT>::all, 1)
       if (cut >= 0) {
         // this CTA's part to its slot; the last CTA of a tile (its rank's rows)
         // adds up the others'
+        if (!OS2_DBG_GUARD(cut < j.rest && pair < j.workers, status)) return true;
         int *mine = j.slots + (((size_t)pair * 2 + slot_of(j, pair, cut)) * 2 + rank) * NT * 128;
 #pragma unroll
         for (int i = 0; i < COLS; i += 4)
@@ -368,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Threads<NT>::all, 1)
         }
       }
       const int ch = tc * 2 * kHalf + (int)rank * kHalf + r_cta;
-      const bool in = ch < j.n;
+      const bool in = ch < j.n && OS2_DBG_GUARD(ch >= 0 && j.ldy >= j.n, status);
       const float sb = in ? j.sb[ch] : 0.f, b = in && j.bias ? j.bias[ch] : 0.f;
       const int left = in ? j.m - tok0 : 0;
       __syncwarp();
@@ -420,8 +423,8 @@ cudaError_t launch(const I8Args &a, cudaStream_t s) {
       !make_map(&mt, a.tokens, false, a.k, a.m, a.pitch, false, NT / 2))
     return cudaErrorInvalidValue;
   i8_fill(j, a);
-  k_i8tc<NT><<<2 * j.workers, Threads<NT>::all, smem_tc<NT>(), s>>>(mw, mt, j, a.status);
-  return cudaGetLastError();
+  return launch_after(k_i8tc<NT>, 2 * j.workers, Threads<NT>::all, smem_tc<NT>(), s, mw, mt, j,
+                      a.status);
 }
 
 // Tokens a tile, by the time of the busiest pair in cycles: about 1350, 1400 and

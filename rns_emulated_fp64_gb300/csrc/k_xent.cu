@@ -371,14 +371,15 @@ struct StoreEpi {
   long ld;
   const int *rowmap;    // or null
   const float *scale;
-  int n;
+  int rows, n;          // of `out`
   bool vec;             // rows of `out` are 16-byte aligned
 
   __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, bool, bool, int m,
-                                       uint8_t *scratch, int *) {
+                                       uint8_t *scratch, int *status) {
     const int lane = threadIdx.x & 31, row0 = row - lane;
     const float s = scale[1];
-    const int mine = row < m ? (rowmap ? rowmap[row] : row) : -1;  // where this lane's row goes
+    int mine = row < m ? (rowmap ? rowmap[row] : row) : -1;  // where this lane's row goes
+    if (!OS2_DBG_GUARD(mine < rows && n <= ld, status)) mine = -1;
 #pragma unroll 1
     for (int g = 0; g < 4; g++) {
       const int left = n - (col0 + g * 32);
@@ -690,12 +691,13 @@ cudaError_t backward(Prep p, const uint16_t *W, long ldw, uint16_t *dW, long ldd
                                               p.status, s)
               : launch_mm2<BF16, false, true>(
                     md, mwt, job,
-                    StoreEpi<BF16>{p.dH, p.lddh, p.rowmap, p.scale, p.k, tma_rows(p.dH, p.lddh)},
+                    StoreEpi<BF16>{p.dH, p.lddh, p.rowmap, p.scale, p.n, p.k,
+                                   tma_rows(p.dH, p.lddh)},
                     p.status, s);
       if (e != cudaSuccess) return e;
     }
     if (dW) {
-      const StoreEpi<BF16> se{dW + (size_t)v0 * lddw, lddw, nullptr, p.scale, p.k,
+      const StoreEpi<BF16> se{dW + (size_t)v0 * lddw, lddw, nullptr, p.scale, vn, p.k,
                               tma_rows(dW, lddw)};
       e = launch_mm2<BF16, true, true>(mdt, mht, Job{vn, p.k, p.n, nullptr, p.count, INT_MAX, 1}, se,
                                        p.status, s);

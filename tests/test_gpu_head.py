@@ -558,6 +558,23 @@ def test_adamw_non_finite_gradients_stay_local():
         assert not bad.any()
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_adamw_8bit_non_finite_blocks(bad):
+    """A non-finite gradient shows in the moments of its block, and in no other."""
+    p, g = torch.ones(1000, device="cuda"), torch.full((1000,), 1e-3, device="cuda")
+    g[300] = bad
+    m, v = torch.zeros(1000, dtype=torch.int8, device="cuda"), torch.zeros(1000, dtype=torch.uint8, device="cuda")
+    am, av = torch.zeros(4, device="cuda"), torch.zeros(4, device="cuda")
+    kw = dict(exp_avg_scales=[am], exp_avg_sq_scales=[av])
+    os2.adamw([p], [g], [m], [v], step=1, lr=1e-3, **kw)
+    mm, vv = os2.adamw_moments(m, am, v, av)
+    for x in (mm, vv):
+        assert torch.isfinite(x[:256]).all() and torch.isfinite(x[512:]).all()
+        assert not torch.isfinite(x[256:512]).any()
+    os2.adamw([p], [torch.full_like(g, 1e-3)], [m], [v], step=2, lr=1e-3, **kw)
+    assert torch.isnan(p[256:512]).all() and torch.isfinite(p[:256]).all() and torch.isfinite(p[512:]).all()
+
+
 def test_adamw_large_tensor_offsets():
     """Elements past 2^31: the last ones are updated like the first."""
     n = (1 << 31) + 1000

@@ -13,9 +13,10 @@ synchronises.  Every tensor of a call lives on one CUDA device.
 """
 from __future__ import annotations
 
+import array
 import contextlib
-import ctypes as ct
 import operator
+import threading
 
 import torch
 
@@ -79,13 +80,27 @@ def _out(out, like, shape, dtype, name="out"):
     return out, max(out.stride(0) if shape[0] > 1 else 0, shape[1], 1)
 
 
-def _workspace(workspace, need, like):
-    """The workspace's address and size (a new one stays alive in the caller)."""
-    if workspace is None:
-        return torch.empty(need or 1, dtype=torch.uint8, device=like.device)
-    if workspace.device != like.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {like.device}")
-    return workspace
+_KEEP = 32 << 20           # bytes of a workspace that is kept for the next call
+_kept = threading.local()  # of a thread: {(device, stream): workspace}
+
+
+def _workspace(workspace, need, like, index):
+    """The call's workspace: the caller's, or one of the binding's own.  Small ones
+    are kept, one for each thread, device and stream (calls that share one are
+    ordered by the stream), because an allocation between two launches costs as
+    much host time as a launch; a captured call gets its own."""
+    if workspace is not None:
+        if workspace.device != like.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {like.device}")
+        return workspace
+    if need > _KEEP or torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    kept, key = _kept.__dict__, (index, _raw_stream(index))
+    ws = kept.get(key)
+    if ws is None or ws.numel() < need:
+        size = min(_KEEP, max(1 << 20, 2 * need))
+        ws = kept[key] = torch.empty(size, dtype=torch.uint8, device=like.device)
+    return ws
 
 
 def _nbytes(t):
@@ -127,7 +142,7 @@ def _i8(X, m, k, ldx, a_scale, Bt, b_scale, bias, out_dtype, out, workspace, str
             bias = _vector(bias, "bias", n, torch.float32, index)
         out, ldc = _out(out, X, (m, n), out_dtype)
         bp = Bt.data_ptr()
-        ws = _workspace(workspace, L.os2_i8gemm_workspace_size(m, n, k, bp, ldb), X)
+        ws = _workspace(workspace, L.os2_i8gemm_workspace_size(m, n, k, bp, ldb), X, index)
         rest = (bp, ldb, b_scale.data_ptr(), None if bias is None else bias.data_ptr(),
                 out.data_ptr(), ldc, _DTYPE[out_dtype], ws.data_ptr(), _nbytes(ws),
                 _raw_stream(index))
@@ -190,7 +205,7 @@ def xent(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, ignore_index: i
         loss = torch.empty(n, dtype=torch.float32, device=dev)
         lse = torch.empty(n, dtype=torch.float32, device=dev)
         wp = W.data_ptr()
-        ws = _workspace(workspace, L.os2_xent_workspace_size(n, k, v, wp, ldw, 0), H)
+        ws = _workspace(workspace, L.os2_xent_workspace_size(n, k, v, wp, ldw, 0), H, index)
         _check(L.os2_xent(n, k, v, _DTYPE[H.dtype], H.data_ptr(), ldh, wp, ldw, labels.data_ptr(),
                           int(ignore_index), loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
                           _nbytes(ws), _raw_stream(index)), "os2_xent")
@@ -212,7 +227,7 @@ def xent_backward(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, lse: t
         dh = torch.empty((n, k), dtype=dt, device=dev) if need_dh else None
         dw = torch.empty((v, k), dtype=dt, device=dev) if need_dw else None
         wp = W.data_ptr()
-        ws = _workspace(workspace, L.os2_xent_workspace_size(n, k, v, wp, ldw, 1), H)
+        ws = _workspace(workspace, L.os2_xent_workspace_size(n, k, v, wp, ldw, 1), H, index)
         _check(L.os2_xent_backward(n, k, v, _DTYPE[H.dtype], H.data_ptr(), ldh, wp, ldw,
                                    labels.data_ptr(), int(ignore_index), lse.data_ptr(),
                                    grad.data_ptr(), None if dh is None else dh.data_ptr(), k,
@@ -245,7 +260,11 @@ _dtype_of, _shape_of = operator.attrgetter("dtype"), operator.attrgetter("shape"
 
 
 def _pointers(ts):
-    return (ct.c_void_p * len(ts))(*map(torch.Tensor.data_ptr, ts))
+    return array.array("Q", map(torch.Tensor.data_ptr, ts))
+
+
+def _address(a):
+    return None if a is None else a.buffer_info()[0]
 
 
 def _list(ts, name, shapes, index, dtypes):
@@ -297,9 +316,10 @@ def adamw(params, grads, exp_avg, exp_avg_sq, *, step: int, lr: float, beta1: fl
                                  f"{ADAMW_BLOCK} elements")
         scales = _pointers(exp_avg_scales), _pointers(exp_avg_sq_scales)
     with _on(index, stream):
-        _check(load().os2_adamw(len(params), (ct.c_longlong * len(params))(*sizes),
-                                _pointers(params), _pointers(grads), _pointers(exp_avg),
-                                _pointers(exp_avg_sq), *scales, _DTYPE[pt], _DTYPE[gt],
+        # host arrays, read before the call returns
+        arrays = [array.array("q", sizes), *map(_pointers, (params, grads, exp_avg, exp_avg_sq)),
+                  *scales]
+        _check(load().os2_adamw(len(params), *map(_address, arrays), _DTYPE[pt], _DTYPE[gt],
                                 8 if q8 else 32, lr, beta1, beta2, eps, weight_decay, int(step),
                                 _raw_stream(index)), "os2_adamw")
 

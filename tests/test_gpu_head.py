@@ -642,6 +642,39 @@ def test_calls_on_another_stream():
     assert (p != 1).all()
 
 
+def test_calls_from_several_threads():
+    """Threads that share a stream do not share a workspace, streams neither: every
+    call's result is its own."""
+    import threading
+    x = [randn(gen(30 + i), 5 + 30 * i, 640) for i in range(4)]
+    wq, sb = os2.quantize_rows(randn(gen(40), 700, 640))
+    h, w, y, _ = xent_case(60, 128, 900, torch.bfloat16, 0.2, 41)
+    want = [os2.i8linear(v, wq, sb) for v in x]
+    base = os2.xent(h, w, y)[0]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i, stream):
+        for _ in range(50):
+            if not torch.equal(os2.i8linear(x[i], wq, sb, stream=stream), want[i]):
+                bad.append(i)
+            if not torch.equal(os2.xent(h, w, y, stream=stream)[0], base):
+                bad.append(-1)
+
+    s = torch.cuda.Stream()
+
+    def run(i):
+        with torch.cuda.stream(s if i < 2 else torch.cuda.Stream()):
+            work(i, None)
+
+    ts = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad
+
+
 def test_repeats_are_bit_identical():
     h, w, y, grad = xent_case(700, 300, 3000, torch.bfloat16, 0.2, 20)
     x = randn(gen(21), 70, 1500).bfloat16()

@@ -22,7 +22,7 @@ struct I8Sizes {
   size_t slot_ints;
 };
 // k_i8few: m <= kI8Few tokens, mma.sync, no slots or counters; k_i8tc: tcgen05.
-constexpr int kI8Few = 32;
+constexpr int kI8Few = 64;
 cudaError_t launch_i8few(const I8Args &a, cudaStream_t s);
 I8Sizes i8tc_sizes(int m, int n, int k);
 cudaError_t launch_i8tc(const I8Args &a, cudaStream_t s);

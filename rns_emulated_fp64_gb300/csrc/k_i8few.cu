@@ -305,13 +305,16 @@ cudaError_t launch(const I8Args &a, cudaStream_t s) {
                         a.overlap, s, mw, mt, j, a.status);
 }
 
-int groups(int m) { return m <= 8 ? 1 : m <= 16 ? 2 : 4; }
+int groups(int m) { return m <= 8 ? 1 : m <= 16 ? 2 : m <= 32 ? 4 : 8; }
 
 }  // namespace
 
 cudaError_t launch_i8few(const I8Args &a, cudaStream_t s) {
   const int g = groups(a.m);
-  return g == 1 ? launch<1>(a, s) : g == 2 ? launch<2>(a, s) : launch<4>(a, s);
+  return g == 1   ? launch<1>(a, s)
+         : g == 2 ? launch<2>(a, s)
+         : g == 4 ? launch<4>(a, s)
+                  : launch<8>(a, s);
 }
 
 // ------------------------------------------------------------- cluster sizes

@@ -413,8 +413,9 @@ cudaError_t launch(const I8Args &a, cudaStream_t s) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(k_i8tc<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)smem_tc<NT>());
+    using T = Threads<NT>;
+    attr_err = set_up(k_i8tc<NT>, smem_tc<NT>(), T::all,
+                      128 * T::r_misc + 256 * T::r_epi + T::conv * T::r_conv);
   });
   if (attr_err != cudaSuccess) return attr_err;
   I8Job j = i8_plan<2 * kHalf>(a.m, a.n, a.k, NT, pairs());

@@ -363,14 +363,27 @@ cudaError_t launch_after(void (*kernel)(P...), int grid, int block, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
+// Sets a kernel's shared memory, and checks that the block is launched with at
+// least the registers that its roles take: a larger sum would wait for ever.
+template <class K>
+cudaError_t set_up(K *kernel, size_t smem, int threads, int registers) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  const cudaError_t f = cudaFuncGetAttributes(&fa, kernel);
+  if (f != cudaSuccess) return f;
+  return fa.numRegs * threads < registers ? cudaErrorInvalidConfiguration : cudaSuccess;
+}
+
 template <bool BF16, bool A_MN, bool B_MN, class Epi>
 cudaError_t launch_mm2(const CUtensorMap &ma, const CUtensorMap &mb, const Job &job,
                        const Epi &epi, int *status, cudaStream_t s) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(k_mm2<BF16, A_MN, B_MN, Epi>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    attr_err = set_up(k_mm2<BF16, A_MN, B_MN, Epi>, kSmem, kThreads,
+                      128 * kRegsMisc + 256 * kRegsEpi);
   });
   if (attr_err != cudaSuccess) return attr_err;
   const long jobs = (long)((job.m + 2 * kHalf - 1) / (2 * kHalf)) * ((job.n + kBN - 1) / kBN) *

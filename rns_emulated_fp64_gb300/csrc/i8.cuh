@@ -32,20 +32,19 @@ namespace os2i8 {
 using namespace os2mm;
 
 // The work: tiles of CH channels x NT tokens over stages of 128 terms.  Whole
-// tiles go round the workers; the last one or two per worker are cut along k as
-// well, so that all end together and few tiles still use all SMs.
+// tiles go round the workers; those that are left over after the last whole wave
+// are cut along k into `parts` for as many workers.
 struct I8Job {
   int m, n;            // tokens, channels
   int tiles_c, tiles_t, stages;  // tiles of channels and tokens, stages of 128 terms
-  int waves;           // whole tiles of each worker (CTA, or pair of them)
-  int rest;            // tiles cut along k
-  int workers;
-  int few, more;       // units of a worker in the cut tiles: unit_begin
+  int workers;         // pairs of CTAs
+  int waves;           // whole tiles of each worker
+  int rest, parts;     // tiles left over, parts of each (rest * parts <= workers)
   int out_dtype;
   const float *sa, *sb, *bias;
   void *y;
   long ldy;
-  int *slots;          // [workers][2][2 CTAs][NT / 4][128][4] partial sums
+  int *slots;          // [workers][2 CTAs][NT / 4][128][4] partial sums
   unsigned *done;      // [rest][2] stages finished, zero before the launch
 };
 
@@ -60,56 +59,28 @@ __device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
   hi = add2(__byte_perm(x, 0x64646464u, 0x4342), 0xE480E480u);
 }
 
-// First unit (stage of a cut tile) of worker p: `few` + 1 units for the first
-// `more` workers, `few` for the others.
-__device__ __forceinline__ int unit_begin(const I8Job &j, int p) {
-  return p * j.few + min(p, j.more);
-}
-// The worker whose range holds unit u.
-__device__ __forceinline__ int worker_of(const I8Job &j, int u) {
-  const int big = j.more * (j.few + 1);
-  return u < big ? u / (j.few + 1) : j.more + (u - big) / j.few;
-}
-
 // The segments of a worker, in order: f(tile, first stage, end stage, index of the
 // cut tile or -1 for a whole one).  Every role walks the same.
 template <class F>
 __device__ __forceinline__ void for_segments(const I8Job &j, int worker, F &&f) {
-  const int u1 = unit_begin(j, worker + 1);
-  int w = 0;
-  for (int u = unit_begin(j, worker); w < j.waves || u < u1;) {
-    int t, s0 = 0, s1 = j.stages, cut = -1;
-    if (w < j.waves) {
-      t = w++ * j.workers + worker;
-    } else {
-      const int r = u / j.stages;
-      s0 = u - r * j.stages;
-      s1 = min(j.stages, s0 + u1 - u);
-      u += s1 - s0;
+  const int last = worker < j.rest * j.parts ? 1 : 0;
+  for (int w = 0; w < j.waves + last; w++) {
+    int t = w * j.workers + worker, s0 = 0, s1 = j.stages, cut = -1;
+    if (w == j.waves) {
+      const int r = worker / j.parts, part = worker - r * j.parts;
       t = j.waves * j.workers + r;
-      if (s1 - s0 < j.stages) cut = r;
+      s0 = part * j.stages / j.parts;
+      s1 = (part + 1) * j.stages / j.parts;
+      if (j.parts > 1) cut = r;
     }
     if (!f(t, s0, s1, cut)) return;
   }
-}
-
-// The part of worker p in cut tile r is its first segment there (slot 0) unless
-// its range began in an earlier tile (slot 1).
-__device__ __forceinline__ int slot_of(const I8Job &j, int p, int r) {
-  return unit_begin(j, p) >= r * j.stages ? 0 : 1;
 }
 
 __device__ __forceinline__ void store_y(void *y, int dtype, size_t i, float v) {
   if (dtype == OS2_F32) static_cast<float *>(y)[i] = v;
   else if (dtype == OS2_BF16) static_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
   else static_cast<__half *>(y)[i] = __float2half_rn(v);
-}
-
-// The other workers that hold parts of cut tile `r` are [first, last] less `me`.
-// Only the first may have begun in an earlier tile (slot 1).
-__device__ __forceinline__ void parts_of(const I8Job &j, int r, int &first, int &last) {
-  first = worker_of(j, r * j.stages);
-  last = worker_of(j, (r + 1) * j.stages - 1);
 }
 
 // How the eight warps of a CTA that hold a part of a cut tile learn whether it
@@ -141,28 +112,7 @@ __device__ __forceinline__ int last_part(I8Join &jn, unsigned *counter, int mine
   const bool ok = mbar_wait_bounded(jn.b, jn.parity, s_abort, kWaitLimit);
   jn.parity ^= 1;
   if (!__all_sync(0xffffffffu, ok)) return -1;
-  __threadfence();
-  return *jn.last ? 1 : 0;
-}
-
-template <int CH>
-I8Job i8_plan(int m, int n, int k, int nt, int workers) {
-  I8Job j = {};
-  j.m = m;
-  j.n = n;
-  j.tiles_c = (n + CH - 1) / CH;
-  j.tiles_t = (m + nt - 1) / nt;
-  j.stages = std::max((k + kStageK - 1) / kStageK, 1);
-  const long tiles = (long)j.tiles_c * j.tiles_t;
-  j.workers = (int)std::max<long>(1, std::min<long>(workers, tiles * j.stages));
-  // a remainder of tiles takes the last whole wave with it, so that a cut tile
-  // has few parts
-  j.waves = (int)(tiles / j.workers) - (tiles % j.workers && tiles >= j.workers ? 1 : 0);
-  j.rest = (int)(tiles - (long)j.waves * j.workers);
-  const int units = j.rest * j.stages;  // fewer than 2 workers * 1024
-  j.few = units / j.workers;
-  j.more = units % j.workers;
-  return j;
+  return *jn.last ? 1 : 0;  // (the parts are read past L1, after the elected thread's fence)
 }
 
 inline void i8_fill(I8Job &j, const I8Args &a) {

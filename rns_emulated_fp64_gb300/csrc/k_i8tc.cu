@@ -18,10 +18,11 @@
 // as A, with less traffic; but such an MMA took 125 cycles or more whatever its N.
 //
 // A CTA pair computes 256 channels x NT tokens.  Whole tiles go round the pairs;
-// the last one or two per pair are cut along k as well, so that all pairs end
-// together and few tiles still use all SMs.  A pair that has part of a tile writes
-// its int32 sums to its own slot, and the CTA that ends a tile last adds the slots
-// up: integers, so in any order the same result.
+// those left over may be cut along k, where the time saved is more than the 4 to
+// 10 us of joining them (plan): a pair then writes its int32 sums to its slot, and
+// the CTA that ends a tile last adds the slots up: integers, so in any order the
+// same result.  (Dealing all stages out evenly, with up to two cut tiles a pair, took 30.5
+// us instead of 25 for 256 x 4096 x 4096, and 47 instead of 33 for 1024 tokens.)
 //
 // Warps: 0 weights by TMA, 1 MMA, 2 tokens by TMA, 4-11 epilogue (its int32 sums
 // take up to 128 registers a thread), 12 and up widening; each role has the registers
@@ -345,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Threads<NT>::all, 1)
         // this CTA's part to its slot; the last CTA of a tile (its rank's rows)
         // adds up the others'
         if (!OS2_DBG_GUARD(cut < j.rest && pair < j.workers, status)) return true;
-        int *mine = j.slots + (((size_t)pair * 2 + slot_of(j, pair, cut)) * 2 + rank) * NT * 128;
+        int *mine = j.slots + ((size_t)pair * 2 + rank) * NT * 128;
 #pragma unroll
         for (int i = 0; i < COLS; i += 4)
           __stcg(reinterpret_cast<int4 *>(mine) + (half * COLS + i) / 4 * 128 + r_cta,
@@ -354,11 +355,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Threads<NT>::all, 1)
                                    threadIdx.x == 4 * 32, s_abort);
         if (last < 0) return gave_up();
         if (!last) return true;
-        int p0, p1;
-        parts_of(j, cut, p0, p1);
-        for (int p = p0; p <= p1; p++) {
+        for (int p = cut * j.parts; p < (cut + 1) * j.parts; p++) {
           if (p == pair) continue;
-          const int *o = j.slots + (((size_t)p * 2 + slot_of(j, p, cut)) * 2 + rank) * NT * 128;
+          const int *o = j.slots + ((size_t)p * 2 + rank) * NT * 128;
 #pragma unroll
           for (int i = 0; i < COLS; i += 4) {
             const int4 v = __ldcg(reinterpret_cast<const int4 *>(o) + (half * COLS + i) / 4 * 128 + r_cta);
@@ -406,10 +405,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Threads<NT>::all, 1)
   }
 }
 
-int pairs() { return std::max(os2_sm_count() / 2, 1); }
+// The tiles of nt tokens, how the ones left over are cut, and the time in cycles: a
+// stage takes about 1350 (64 and 128 tokens: the widening bounds it) or 1450 (256);
+// joining takes 5000, writing a part 700 for every 64 tokens, and reading another
+// part 1300.  (At 256 x 4096 x 4096, where those were measured.)
+I8Job plan(int m, int n, int k, int nt, double *cycles) {
+  I8Job j = {};
+  j.m = m;
+  j.n = n;
+  j.tiles_c = (n + 2 * kHalf - 1) / (2 * kHalf);
+  j.tiles_t = (m + nt - 1) / nt;
+  j.stages = (k + kStageK - 1) / kStageK;
+  const long tiles = (long)j.tiles_c * j.tiles_t;
+  j.workers = (int)std::min<long>(std::max(os2_sm_count() / 2, 1), tiles);
+  j.waves = (int)(tiles / j.workers);
+  j.rest = (int)(tiles - (long)j.waves * j.workers);
+  const int all = std::max(os2_sm_count() / 2, 1);
+  if (tiles < all) {  // no whole wave: all tiles may be cut
+    j.waves = 0;
+    j.rest = (int)tiles;
+    j.workers = all;
+  }
+  const double stage = nt == 256 ? 1450 : 1350;
+  double least = 1e30;
+  for (int parts = 1; j.rest && parts <= j.workers / j.rest && parts <= j.stages; parts++) {
+    const double t = stage * ((j.stages + parts - 1) / parts) +
+                     (parts > 1 ? 5000 + nt / 64 * (700 + 1300. * (parts - 1)) : 0);
+    if (t < least) {
+      least = t;
+      j.parts = parts;
+    }
+  }
+  if (!j.rest) {
+    j.parts = 1;
+    least = 0;
+  }
+  if (!j.waves) j.workers = j.rest * j.parts;
+  *cycles = stage * j.waves * j.stages + least;
+  return j;
+}
+
+// The tile width with the least time.
+I8Job plan(int m, int n, int k, int *nt) {
+  I8Job best = {};
+  double least = 1e30;
+  for (const int w : {64, 128, 256}) {
+    double t;
+    const I8Job j = plan(m, n, k, w, &t);
+    if (t < least) {
+      least = t;
+      best = j;
+      *nt = w;
+    }
+  }
+  return best;
+}
 
 template <int NT>
-cudaError_t launch(const I8Args &a, cudaStream_t s) {
+cudaError_t launch(const I8Args &a, I8Job j, cudaStream_t s) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
@@ -418,7 +471,6 @@ cudaError_t launch(const I8Args &a, cudaStream_t s) {
                       128 * T::r_misc + 256 * T::r_epi + T::conv * T::r_conv);
   });
   if (attr_err != cudaSuccess) return attr_err;
-  I8Job j = i8_plan<2 * kHalf>(a.m, a.n, a.k, NT, pairs());
   CUtensorMap mw, mt;
   if (!map_w(&mw, a.W, a.k, a.n, a.ldw) ||
       !make_map(&mt, a.tokens, false, a.k, a.m, a.pitch, false, NT / 2))
@@ -428,37 +480,16 @@ cudaError_t launch(const I8Args &a, cudaStream_t s) {
                       a.status);
 }
 
-// Tokens a tile, by the time of the busiest pair in cycles: about 1350, 1400 and
-// 1500 a stage of 64, 128 and 256 tokens (nearly the same: the widening bounds
-// it), and for a cut tile 3000 and 350 for every 8 columns of another part.
-int tile_tokens(int m, int n, int k) {
-  int best = 64;
-  double least = 1e30;
-  for (const int nt : {64, 128, 256}) {
-    const I8Job j = i8_plan<2 * kHalf>(m, n, k, nt, pairs());
-    double t = (double)(nt == 64 ? 1350 : nt == 128 ? 1400 : 1500) *
-               ((double)j.waves * j.stages + j.few + (j.more > 0));
-    if (j.rest && j.few + (j.more > 0) < j.rest * j.stages && j.few % j.stages) {
-      const double parts = std::min<double>(j.stages, (double)j.stages / std::max(j.few, 1));
-      t += 3000 + 350. * (nt / 16) * std::max(1., parts);
-    }
-    if (t < least) {
-      least = t;
-      best = nt;
-    }
-  }
-  return best;
-}
-
 }  // namespace
 
 I8Sizes i8tc_sizes(int m, int n, int k) {
-  const int nt = tile_tokens(m, n, k);
-  const I8Job j = i8_plan<2 * kHalf>(m, n, k, nt, pairs());
-  return {2 * j.rest, j.rest ? (size_t)j.workers * 4 * nt * 128 : 0};
+  int nt;
+  const I8Job j = plan(m, n, k, &nt);
+  return {j.parts > 1 ? 2 * j.rest : 0, j.parts > 1 ? (size_t)j.workers * 2 * nt * 128 : 0};
 }
 
 cudaError_t launch_i8tc(const I8Args &a, cudaStream_t s) {
-  const int nt = tile_tokens(a.m, a.n, a.k);
-  return nt == 64 ? launch<64>(a, s) : nt == 128 ? launch<128>(a, s) : launch<256>(a, s);
+  int nt;
+  const I8Job j = plan(a.m, a.n, a.k, &nt);
+  return nt == 64 ? launch<64>(a, j, s) : nt == 128 ? launch<128>(a, j, s) : launch<256>(a, j, s);
 }

@@ -273,7 +273,9 @@ struct StatsEpi {
   }
 
   __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, bool first,
-                                       bool last, int m, uint8_t *, int *status) {
+                                       bool last, int m, const CUtensorMap *, uint8_t *,
+                                       int *status) {
+    if (row - (int)(threadIdx.x & 31) >= m) return;  // no row of this warp
     const int y = row < m ? label[row] - col0 : -1;
     float top = -INFINITY, sum = 0.f;
     if (CHUNKED) {
@@ -309,6 +311,7 @@ struct StatsEpi {
     if (row < m && OS2_DBG_GUARD((col0 >> 7) < parts, status))
       part[(size_t)row * parts + (col0 >> 7)] = make_float2(top, sum);
   }
+  __device__ __forceinline__ void finish() {}
 };
 
 // Backward: D of one piece (columns v0 .. v0 + v) in the operands' type.  Its
@@ -324,7 +327,15 @@ struct GradEpi {
   int v0, v;
 
   __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, bool, bool, int m,
-                                       uint8_t *, int *) {
+                                       const CUtensorMap *, uint8_t *, int *) {
+    const int row0 = row - (int)(threadIdx.x & 31);
+    uint4 *dst = reinterpret_cast<uint4 *>(d + (size_t)row * pitch + col0);
+    if (row0 >= m) {  // no row of this warp: zeros, as far as the last stage of D^T H reads
+      if (row0 < (m + kStageK - 1) / kStageK * kStageK)
+#pragma unroll
+        for (int q = 0; q < 16; q++) dst[q] = make_uint4(0, 0, 0, 0);
+      return;
+    }
     const bool in = row < m;
     const int y = in ? label[row] - v0 - col0 : -1;
     // 2^E p = 2^(z log2 e - lse log2 e + E), so that p's own range does not cut it
@@ -332,7 +343,6 @@ struct GradEpi {
     constexpr float c = (float)(1ull << E);
     const float l = in ? fmaf(lse[row], kLog2e, -(float)E) : 0.f;
     const float gr = in ? grad[row] * scale[0] : 0.f;
-    uint4 *dst = reinterpret_cast<uint4 *>(d + (size_t)row * pitch + col0);
 #pragma unroll 1
     for (int g = 0; g < 4; g++) {
       uint32_t r[32];
@@ -358,14 +368,16 @@ struct GradEpi {
                                     pack2<BF16>(x[8 * q + 6], x[8 * q + 7]));
     }
   }
+  __device__ __forceinline__ void finish() {}
 };
 
 // dW, and dH where it comes out of one product: scaled back, rounded once, to the
-// row that a packed row came from.  The rows go through shared memory, so that a
-// store instruction writes eight rows' 64 bytes (a lane's own row directly, 16 bytes
-// of 32 rows at a time: 94 us instead of 88 for dW of 32000 x 2048 from 8 rows, and
-// 719 instead of 223 where the rows are not aligned).
-template <bool BF16>
+// row that a packed row came from.  Written straight from a lane's own row, 16 bytes
+// of 32 rows at a time, dW of 32000 x 2048 from 8 rows took 55 us, 719 with rows that
+// are not aligned.  So the rows go through shared memory: dW's 32 x 32 blocks leave
+// by TMA (DW and aligned rows), two of them on their way while the next is made; else
+// eight rows' 64 bytes an instruction, or one row's where rows are not aligned.
+template <bool BF16, bool TMA>
 struct StoreEpi {
   uint16_t *out;
   long ld;
@@ -375,7 +387,7 @@ struct StoreEpi {
   bool vec;             // rows of `out` are 16-byte aligned
 
   __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, bool, bool, int m,
-                                       uint8_t *scratch, int *status) {
+                                       const CUtensorMap *mapD, uint8_t *scratch, int *status) {
     const int lane = threadIdx.x & 31, row0 = row - lane;
     const float s = scale[1];
     int mine = row < m ? (rowmap ? rowmap[row] : row) : -1;  // where this lane's row goes
@@ -388,35 +400,57 @@ struct StoreEpi {
       __syncwarp();
       tmem_ld32(taddr + g * 32, r);
       tmem_wait_ld();
-      float x[32];
+      uint4 v[4];
 #pragma unroll
-      for (int i = 0; i < 32; i++) x[i] = __uint_as_float(r[i]) * s;
+      for (int q = 0; q < 4; q++) {
+        uint32_t w[4];
 #pragma unroll
-      for (int q = 0; q < 4; q++)
-        *reinterpret_cast<uint4 *>(scratch + lane * 80 + q * 16) =
-            make_uint4(pack2<BF16>(x[8 * q], x[8 * q + 1]), pack2<BF16>(x[8 * q + 2], x[8 * q + 3]),
-                       pack2<BF16>(x[8 * q + 4], x[8 * q + 5]),
-                       pack2<BF16>(x[8 * q + 6], x[8 * q + 7]));
-      __syncwarp();
-      uint16_t *dst = out + col0 + g * 32;
-      if (left >= 32 && vec) {
+        for (int i = 0; i < 4; i++)
+          w[i] = pack2<BF16>(__uint_as_float(r[8 * q + 2 * i]) * s,
+                             __uint_as_float(r[8 * q + 2 * i + 1]) * s);
+        v[q] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if constexpr (TMA) {
+        uint8_t *block = scratch + (g & 1) * 2048;
+        if (lane == 0) bulk_wait_read<1>();  // the block before the last has left
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int rr = i * 8 + (lane >> 2), to = __shfl_sync(0xffffffffu, mine, rr);
-          if (to >= 0)
-            reinterpret_cast<uint4 *>(dst + (size_t)to * ld)[lane & 3] =
-                *reinterpret_cast<const uint4 *>(scratch + rr * 80 + (lane & 3) * 16);
+        for (int q = 0; q < 4; q++)
+          *reinterpret_cast<uint4 *>(block + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) = v[q];
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(mapD, block, col0 + g * 32, row0, 0);  // rows from m on are cut off by the map
+          bulk_commit();
         }
       } else {
+#pragma unroll
+        for (int q = 0; q < 4; q++) *reinterpret_cast<uint4 *>(scratch + lane * 80 + q * 16) = v[q];
+        __syncwarp();
+        uint16_t *dst = out + col0 + g * 32;
+        if (left >= 32 && vec) {
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int rr = i * 8 + (lane >> 2), to = __shfl_sync(0xffffffffu, mine, rr);
+            if (to >= 0)
+              reinterpret_cast<uint4 *>(dst + (size_t)to * ld)[lane & 3] =
+                  *reinterpret_cast<const uint4 *>(scratch + rr * 80 + (lane & 3) * 16);
+          }
+        } else {
 #pragma unroll 8
-        for (int rr = 0; rr < 32; rr++) {
-          const int to = __shfl_sync(0xffffffffu, mine, rr);
-          if (to >= 0 && lane < left)
-            dst[(size_t)to * ld + lane] =
-                *reinterpret_cast<const uint16_t *>(scratch + rr * 80 + lane * 2);
+          for (int rr = 0; rr < 32; rr++) {
+            const int to = __shfl_sync(0xffffffffu, mine, rr);
+            if (to >= 0 && lane < left)
+              dst[(size_t)to * ld + lane] =
+                  *reinterpret_cast<const uint16_t *>(scratch + rr * 80 + lane * 2);
+          }
         }
       }
     }
+  }
+  __device__ __forceinline__ void finish() {
+    if (TMA && (threadIdx.x & 31) == 0) bulk_wait_all();
+    __syncwarp();
   }
 };
 
@@ -428,7 +462,7 @@ struct SumEpi {
   bool add;
 
   __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int split, bool, bool,
-                                       int m, uint8_t *, int *) {
+                                       int m, const CUtensorMap *, uint8_t *, int *) {
     const bool in = row < m;
     float4 *a = reinterpret_cast<float4 *>(acc + ((size_t)split * rows + (in ? row : 0)) * pitch + col0);
 #pragma unroll 1
@@ -453,9 +487,11 @@ struct SumEpi {
       }
     }
   }
+  __device__ __forceinline__ void finish() {}
 };
 
-// dH from those sums, the parts in their order.
+// dH from those sums, the parts in their order: four columns a thread, eight parts
+// on their way at once.
 template <bool BF16>
 __global__ void __launch_bounds__(256)
     k_dh_join(const int *count, const int *rowmap, const float *scale, const float *acc, int splits,
@@ -463,28 +499,33 @@ __global__ void __launch_bounds__(256)
   next_may_start();
   wait_for_previous();
   const float s = scale[1];
-  const long per = pitch / 8, total = per * *count;
+  const int per = (k + 3) / 4;
+  const long total = (long)per * *count;
   for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
     const long row = i / per;
-    const int h = (int)(i - row * per) * 8;
-    if (h >= k) continue;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int p = 0; p < splits; p++) {
-      const float4 *a = reinterpret_cast<const float4 *>(acc + ((size_t)p * rows + row) * pitch + h);
-      const float4 u = a[0], v = a[1];
-      x[0] += u.x, x[1] += u.y, x[2] += u.z, x[3] += u.w;
-      x[4] += v.x, x[5] += v.y, x[6] += v.z, x[7] += v.w;
-    }
-    uint16_t *dst = out + (size_t)rowmap[row] * ld + h;
-    if (vec && h + 8 <= k) {
-      *reinterpret_cast<uint4 *>(dst) =
-          make_uint4(pack2<BF16>(x[0] * s, x[1] * s), pack2<BF16>(x[2] * s, x[3] * s),
-                     pack2<BF16>(x[4] * s, x[5] * s), pack2<BF16>(x[6] * s, x[7] * s));
-    } else {
+    const int h = (int)(i - row * per) * 4;
+    const float *a = acc + (size_t)row * pitch + h;
+    const int to = rowmap[row];
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < splits; p0 += 8) {
+      float4 v[8];
 #pragma unroll
-      for (int e = 0; e < 8; e++)
-        if (h + e < k) dst[e] = pack1<BF16>(x[e] * s);
+      for (int u = 0; u < 8; u++)
+        v[u] = p0 + u < splits
+                   ? __ldg(reinterpret_cast<const float4 *>(a + (size_t)(p0 + u) * rows * pitch))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < 8; u++) x.x += v[u].x, x.y += v[u].y, x.z += v[u].z, x.w += v[u].w;
+    }
+    uint16_t *dst = out + (size_t)to * ld + h;
+    if (vec && h + 4 <= k) {
+      *reinterpret_cast<uint2 *>(dst) =
+          make_uint2(pack2<BF16>(x.x * s, x.y * s), pack2<BF16>(x.z * s, x.w * s));
+    } else {
+      const float e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int q = 0; q < 4; q++)
+        if (h + q < k) dst[q] = pack1<BF16>(e[q] * s);
     }
   }
 }
@@ -691,21 +732,30 @@ cudaError_t backward(Prep p, const uint16_t *W, long ldw, uint16_t *dW, long ldd
                                               p.status, s)
               : launch_mm2<BF16, false, true>(
                     md, mwt, job,
-                    StoreEpi<BF16>{p.dH, p.lddh, p.rowmap, p.scale, p.n, p.k,
+                    StoreEpi<BF16, false>{p.dH, p.lddh, p.rowmap, p.scale, p.n, p.k,
                                    tma_rows(p.dH, p.lddh)},
                     p.status, s);
       if (e != cudaSuccess) return e;
     }
     if (dW) {
-      const StoreEpi<BF16> se{dW + (size_t)v0 * lddw, lddw, nullptr, p.scale, vn, p.k,
-                              tma_rows(dW, lddw)};
-      e = launch_mm2<BF16, true, true>(mdt, mht, Job{vn, p.k, p.n, nullptr, p.count, INT_MAX, 1}, se,
-                                       p.status, s);
+      uint16_t *out = dW + (size_t)v0 * lddw;
+      const Job job{vn, p.k, p.n, nullptr, p.count, INT_MAX, 1};
+      if (tma_rows(dW, lddw)) {
+        CUtensorMap mo;
+        if (!make_store_map(&mo, out, BF16, p.k, vn, lddw)) return cudaErrorInvalidValue;
+        e = launch_mm2<BF16, true, true>(
+            mdt, mht, job, StoreEpi<BF16, true>{out, lddw, nullptr, p.scale, vn, p.k, true}, p.status,
+            s, &mo);
+      } else {
+        e = launch_mm2<BF16, true, true>(
+            mdt, mht, job, StoreEpi<BF16, false>{out, lddw, nullptr, p.scale, vn, p.k, false},
+            p.status, s);
+      }
       if (e != cudaSuccess) return e;
     }
   }
   if (!p.dH || L.pieces * L.splits == 1) return cudaSuccess;
-  const long groups = acc_pitch / 8 * p.n;
+  const long groups = (p.k + 3L) / 4 * p.n;
   return launch_after(k_dh_join<BF16>, (int)std::min<long>((groups + 255) / 256, 16L * os2_sm_count()),
                       256, 0, s, p.count, p.rowmap, p.scale, acc, L.splits, L.npad, acc_pitch, p.k,
                       p.dH, p.lddh, tma_rows(p.dH, p.lddh));

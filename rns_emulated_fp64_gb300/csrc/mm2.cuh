@@ -49,8 +49,8 @@ constexpr int kThreads = 128 + kEpiThreads;
 // registers a thread: 384 x 168 at launch >= 128 x 64 + 256 x 216
 constexpr int kRegsMisc = 64, kRegsEpi = 216;
 static_assert(128 * kRegsMisc + 256 * kRegsEpi <= kThreads * 168, "registers");
-constexpr uint32_t kScratch = 32 * 80;          // an epilogue warp's own shared memory
-constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kOpBytes + 256 + kEpiThreads / 32 * kScratch;
+constexpr uint32_t kScratch = 4096;             // an epilogue warp's own shared memory
+constexpr size_t kSmem = 1024 + (size_t)kStages * 2 * kOpBytes + 512 + kEpiThreads / 32 * kScratch;
 static_assert(kSmem <= 227 * 1024, "shared memory of the product kernel");
 constexpr long long kWaitLimit = 4000000000LL;  // clock cycles (about 2 s)
 
@@ -79,17 +79,19 @@ __device__ __forceinline__ void tile_coords(int t, int tiles_m, int tiles_n, int
 
 // Epi: a copyable struct with
 //   void unit(uint32_t taddr, int row, int col0, int split, bool first, bool last, int m,
-//             uint8_t *scratch, int *status)
+//             const CUtensorMap *mapD, uint8_t *scratch, int *status)
+//   void finish()
 // called by every lane of an epilogue warp (converged) with the TMEM address of
 // its lane quarter's 128 columns, its own row of the output and the first of
 // its 128 columns.  It reads TMEM with tcgen05.ld and waits for the loads; rows
 // from m on and columns past the output are its business.  It may keep state
 // between the chunks of a job (first, last).  scratch: kScratch bytes of the
-// warp's own.
+// warp's own, on a 512-byte boundary; mapD: the output's tensor map, where it has
+// one.  finish is called once, at the end.
 template <bool BF16, bool A_MN, bool B_MN, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_mm2(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-          const Job job, const Epi epi_in, int *status) {
+          const __grid_constant__ CUtensorMap mapD, const Job job, const Epi epi_in, int *status) {
   constexpr uint32_t IDESC = idesc_f16_f32(2 * kHalf, kBN) |
                              (BF16 ? (1u << 7) | (1u << 10) : 0u) | (A_MN ? 1u << 15 : 0u) |
                              (B_MN ? 1u << 16 : 0u);
@@ -272,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * 128;
     const uint32_t empty_leader[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0),
                                       mapa_shared(smem_u32(&acc_empty[1]), 0)};
-    uint8_t *scratch = reinterpret_cast<uint8_t *>(full) + 256 + (warp - 4) * kScratch;
+    uint8_t *scratch = reinterpret_cast<uint8_t *>(full) + 512 + (warp - 4) * kScratch;
     uint32_t aphase[2] = {0, 0};
     int unit = 0;
     bool ok = true;
@@ -296,12 +298,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         aphase[buf] ^= 1;
         tc_fence_after();
         epi.unit(lane_base + (uint32_t)(buf * kBN), row, col0, t / tiles, ks0 == begin, ks1 == end,
-                 m, scratch, status);
+                 m, &mapD, scratch, status);
         tc_fence_before();
         mbar_arrive_remote(empty_leader[buf]);
         ks0 = ks1;
       }
     }
+    epi.finish();
   }
 
   tc_fence_before();
@@ -363,6 +366,21 @@ cudaError_t launch_after(void (*kernel)(P...), int grid, int block, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
+// (A block of 32 x 32 entries of a row-major matrix, as a warp stores it: 64-byte
+// rows in the 64-byte swizzle.)
+inline bool make_store_map(CUtensorMap *map, void *base, bool bf16, long cols, long rows,
+                           long pitch) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
+  cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)pitch * 2 * (cuuint64_t)rows};
+  cuuint32_t box[3] = {32, 32, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base,
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Sets a kernel's shared memory, and checks that the block is launched with at
 // least the registers that its roles take: a larger sum would wait for ever.
 template <class K>
@@ -378,7 +396,8 @@ cudaError_t set_up(K *kernel, size_t smem, int threads, int registers) {
 
 template <bool BF16, bool A_MN, bool B_MN, class Epi>
 cudaError_t launch_mm2(const CUtensorMap &ma, const CUtensorMap &mb, const Job &job,
-                       const Epi &epi, int *status, cudaStream_t s) {
+                       const Epi &epi, int *status, cudaStream_t s,
+                       const CUtensorMap *md = nullptr) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
@@ -390,8 +409,8 @@ cudaError_t launch_mm2(const CUtensorMap &ma, const CUtensorMap &mb, const Job &
                     job.splits;
   if (jobs <= 0) return cudaSuccess;
   const int pairs = (int)std::min<long>(std::max(os2_sm_count() / 2, 1), jobs);
-  return launch_after(k_mm2<BF16, A_MN, B_MN, Epi>, 2 * pairs, kThreads, kSmem, s, ma, mb, job, epi,
-                      status);
+  return launch_after(k_mm2<BF16, A_MN, B_MN, Epi>, 2 * pairs, kThreads, kSmem, s, ma, mb,
+                      md ? *md : ma, job, epi, status);
 }
 
 }  // namespace os2mm

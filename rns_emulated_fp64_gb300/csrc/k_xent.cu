@@ -375,7 +375,7 @@ struct GradEpi {
 // row that a packed row came from.  Written straight from a lane's own row, 16 bytes
 // of 32 rows at a time, dW of 32000 x 2048 from 8 rows took 55 us, 719 with rows that
 // are not aligned.  So the rows go through shared memory: dW's 32 x 32 blocks leave
-// by TMA (DW and aligned rows), two of them on their way while the next is made; else
+// by TMA (aligned rows), two of them on their way while the next is made; else
 // eight rows' 64 bytes an instruction, or one row's where rows are not aligned.
 template <bool BF16, bool TMA>
 struct StoreEpi {

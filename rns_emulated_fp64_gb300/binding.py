@@ -7,6 +7,8 @@ CPU fallback: if the library cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes as ct
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -35,6 +37,7 @@ EXPORTS = ("os2_workspace_size", "os2_gemm", "os2_host_workspace_size", "os2_gem
            "os2_adamw_moments")
 
 _lib = None
+_head = None
 _lock = threading.Lock()
 
 
@@ -136,6 +139,28 @@ def load(build_if_missing: bool = True):
         L.os2_adamw_moments.restype = i
         _lib = L
         return L
+
+
+def load_head():
+    """Load the native part of head.py (built first if it is missing) on the
+    library that ``load`` gives."""
+    global _head
+    if _head is None:
+        L = load()
+        with _lock:
+            if _head is None:
+                path = _build.head_path()
+                if not os.path.exists(path):
+                    _build.build_head()
+                loader = importlib.machinery.ExtensionFileLoader("os2_head", path)
+                m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("os2_head", path, loader=loader))
+                loader.exec_module(m)
+                m.bind(Os2Error, *(ct.cast(f, ct.c_void_p).value for f in (
+                    L.os2_quantize_rows, L.os2_i8gemm_workspace_size, L.os2_i8gemm, L.os2_i8linear,
+                    L.os2_xent_workspace_size, L.os2_xent, L.os2_xent_backward, L.os2_adamw,
+                    L.os2_adamw_moments)))
+                _head = m
+    return _head
 
 
 def status_string(st: int) -> str:

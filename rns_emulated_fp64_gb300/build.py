@@ -2,7 +2,9 @@
 
 Every CUDA source is compiled for sm_103a only, in parallel, then linked into
 one shared library with the CUDA runtime linked statically.  The library has a
-plain C ABI (include/os2.h); the Python binding loads it with ctypes.
+plain C ABI (include/os2.h); the Python binding loads it with ctypes.  Beside it
+goes os2_head.so, the native argument checks of head.py (csrc/py_head.cpp, host
+code built against the installed PyTorch).
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -35,6 +38,37 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def head_path() -> str:
+    """The native part of head.py, for the PyTorch that is installed."""
+    import torch
+    return os.path.join(BUILD, f"os2_head-{torch.__version__}.so")
+
+
+def build_head(force: bool = False) -> str:
+    """Compile (if stale) and return the path of the native part of head.py."""
+    import torch
+    out, src, header = head_path(), os.path.join(CSRC, "py_head.cpp"), os.path.join(ROOT, "include", "os2.h")
+    if not force and not _stale(out, [src, header]):
+        return out
+    os.makedirs(BUILD, exist_ok=True)
+    base = os.path.dirname(torch.__file__)
+    libs = os.path.join(base, "lib")
+    incs = [os.path.join(ROOT, "include"), os.path.join(base, "include"),
+            os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"],
+            os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    tmp = out + f".tmp{os.getpid()}"
+    r = subprocess.run([os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+                        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+                       + [f"-I{d}" for d in incs] + [src, "-o", tmp, f"-L{libs}", "-ltorch_python",
+                       "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{libs}"],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
 def _stale(outputs: str, inputs: list[str]) -> bool:
     if not os.path.exists(outputs):
         return True
@@ -44,13 +78,15 @@ def _stale(outputs: str, inputs: list[str]) -> bool:
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None,
           debug: bool = False) -> str:
-    """Compile (if stale) and return the path of libos2.so (debug: the build
-    with the kernels' index checks, in _build_debug/)."""
+    """Compile (if stale) libos2.so and the native part of head.py, and return the
+    path of libos2.so (debug: the build with the kernels' index checks, in
+    _build_debug/)."""
     bdir, lib = (BUILD_DEBUG, LIB_DEBUG) if debug else (BUILD, LIB)
     os.makedirs(bdir, exist_ok=True)
     headers = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
     srcs = sources()
     if not force and not _stale(lib, srcs + headers + [__file__]):
+        build_head()
         return lib
     cc = nvcc()
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -70,8 +106,10 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(os.cpu_count() or 8, len(srcs)))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(os.cpu_count() or 8, len(srcs) + 1))) as ex:
+        head = ex.submit(build_head, force)
         objs = list(ex.map(compile_one, srcs))
+        head.result()
     tmp = lib + f".tmp{os.getpid()}"
     r = subprocess.run([cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"],
                        capture_output=True, text=True)

@@ -455,39 +455,45 @@ struct StoreEpi {
 };
 
 // dH out of several products (pieces of the vocabulary, parts of one): FP32 sums,
-// one array for each part, added to by each piece.
+// one array for each part, written by the first piece and added to by each further
+// one, in their order.  Like dW's, the blocks leave through shared memory by TMA, which
+// also adds: a lane that wrote (or read and wrote) its own row itself took
+// 16 bytes of 32 rows at a time.
 struct SumEpi {
-  float *acc;           // [splits][rows][pitch], pitch a multiple of 256
-  long rows, pitch;
   bool add;
 
   __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int split, bool, bool,
-                                       int m, const CUtensorMap *, uint8_t *, int *) {
-    const bool in = row < m;
-    float4 *a = reinterpret_cast<float4 *>(acc + ((size_t)split * rows + (in ? row : 0)) * pitch + col0);
+                                       int m, const CUtensorMap *mapD, uint8_t *scratch, int *) {
+    const int lane = threadIdx.x & 31, row0 = row - lane;
+    if (row0 >= m) return;  // no row of this warp (rows past m within it: sums that nothing reads)
 #pragma unroll 1
-    for (int g = 0; g < 4; g++) {
-      float4 av[8];
-      if (add && in) {
-#pragma unroll
-        for (int q = 0; q < 8; q++) av[q] = a[g * 8 + q];
-      }
-      uint32_t r[32];
+    for (int g = 0; g < 8; g++) {
+      uint32_t r[16];
       __syncwarp();
-      tmem_ld32(taddr + g * 32, r);
+      tmem_ld16(taddr + g * 16, r);
       tmem_wait_ld();
-      if (in) {
+      uint8_t *block = scratch + (g & 1) * 2048;
+      if (lane == 0) bulk_wait_read<1>();  // the block before the last has left
+      __syncwarp();
 #pragma unroll
-        for (int q = 0; q < 8; q++) {
-          float4 x = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
-                                 __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
-          if (add) x.x += av[q].x, x.y += av[q].y, x.z += av[q].z, x.w += av[q].w;
-          a[g * 8 + q] = x;
-        }
+      for (int q = 0; q < 4; q++)
+        *reinterpret_cast<uint4 *>(block + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) =
+            make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (add)
+          tma_add_3d(mapD, block, col0 + g * 16, row0, split);
+        else
+          tma_store_3d(mapD, block, col0 + g * 16, row0, split);
+        bulk_commit();
       }
     }
   }
-  __device__ __forceinline__ void finish() {}
+  __device__ __forceinline__ void finish() {
+    if ((threadIdx.x & 31) == 0) bulk_wait_all();
+    __syncwarp();
+  }
 };
 
 // dH from those sums, the parts in their order: four columns a thread, eight parts
@@ -708,9 +714,14 @@ cudaError_t backward(Prep p, const uint16_t *W, long ldw, uint16_t *dW, long ldd
   uint16_t *d = at<uint16_t>(ws, L.d);
   float *acc = at<float>(ws, L.acc);
   const long acc_pitch = (long)os2_round_up((size_t)p.k, 256);
-  CUtensorMap mh, mht, mw, mwt, md, mdt;
+  CUtensorMap mh, mht, mw, mwt, md, mdt, msum;
   if (!make_map(&mh, p.Hc, BF16, p.k, p.n, L.kp, false) ||
       !make_map(&mht, p.Hc, BF16, p.k, L.npad, L.kp, true))
+    return cudaErrorInvalidValue;
+  const bool sums = L.pieces * L.splits > 1;
+  if (p.dH && sums &&
+      !make_store_map(&msum, acc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, acc_pitch, L.npad, acc_pitch,
+                      L.splits))
     return cudaErrorInvalidValue;
   for (int i = 0; i < L.pieces; i++) {
     const int v0 = i * L.vc, vn = std::min(L.vc, p.v - v0);
@@ -727,9 +738,8 @@ cudaError_t backward(Prep p, const uint16_t *W, long ldw, uint16_t *dW, long ldd
     if (p.dH) {
       // (a shorter last piece may have fewer stages than parts: those add nothing)
       const Job job{p.n, p.k, vn, p.count, nullptr, INT_MAX, L.splits};
-      e = L.pieces * L.splits > 1
-              ? launch_mm2<BF16, false, true>(md, mwt, job, SumEpi{acc, L.npad, acc_pitch, i > 0},
-                                              p.status, s)
+      e = sums
+              ? launch_mm2<BF16, false, true>(md, mwt, job, SumEpi{i > 0}, p.status, s, &msum)
               : launch_mm2<BF16, false, true>(
                     md, mwt, job,
                     StoreEpi<BF16, false>{p.dH, p.lddh, p.rowmap, p.scale, p.n, p.k,
@@ -739,10 +749,13 @@ cudaError_t backward(Prep p, const uint16_t *W, long ldw, uint16_t *dW, long ldd
     }
     if (dW) {
       uint16_t *out = dW + (size_t)v0 * lddw;
-      const Job job{vn, p.k, p.n, nullptr, p.count, INT_MAX, 1};
+      // (dW reads D as dH does, and nothing of dH)
+      const Job job{vn, p.k, p.n, nullptr, p.count, INT_MAX, 1, p.dH != nullptr};
       if (tma_rows(dW, lddw)) {
         CUtensorMap mo;
-        if (!make_store_map(&mo, out, BF16, p.k, vn, lddw)) return cudaErrorInvalidValue;
+        if (!make_store_map(&mo, out,
+                            BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                            2, p.k, vn, lddw)) return cudaErrorInvalidValue;
         e = launch_mm2<BF16, true, true>(
             mdt, mht, job, StoreEpi<BF16, true>{out, lddw, nullptr, p.scale, vn, p.k, true}, p.status,
             s, &mo);
@@ -754,7 +767,7 @@ cudaError_t backward(Prep p, const uint16_t *W, long ldw, uint16_t *dW, long ldd
       if (e != cudaSuccess) return e;
     }
   }
-  if (!p.dH || L.pieces * L.splits == 1) return cudaSuccess;
+  if (!p.dH || !sums) return cudaSuccess;
   const long groups = (p.k + 3L) / 4 * p.n;
   return launch_after(k_dh_join<BF16>, (int)std::min<long>((groups + 255) / 256, 16L * os2_sm_count()),
                       256, 0, s, p.count, p.rowmap, p.scale, acc, L.splits, L.npad, acc_pitch, p.k,

@@ -61,6 +61,10 @@ struct Job {
   const int *k_dev;   // if set, the terms that count (<= k); the rest of the last stage is zero
   int chunk;          // stages per accumulation chunk (INT_MAX: the whole of k)
   int splits;         // parts of k, each a job of its own (at most the stages of k; 1 with k_dev)
+  // Set where the launch in front is a product that this one reads nothing from
+  // and that starts after all this one reads is there: it begins on the SMs that
+  // the other leaves free, and ends after it.
+  bool beside = false;
 };
 
 __device__ __forceinline__ void set_status(int *status, int code) {
@@ -140,8 +144,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
 
+  // the next launch may start once all this one reads is there: a `beside` one relies on it
+  if (!job.beside) wait_for_previous();
   next_may_start();
-  wait_for_previous();
   // counts known on the device only, never above the host's
   const int m = job.m_dev ? min(max(*job.m_dev, 0), job.m) : job.m;
   const int k = job.k_dev ? min(max(*job.k_dev, 0), job.k) : job.k;
@@ -307,6 +312,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     epi.finish();
   }
 
+  // what follows waits for this launch alone, so this one ends after the one in front
+  if (job.beside) wait_for_previous();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no CTA leaves while its peer may still touch its shared memory or TMEM
@@ -366,19 +373,19 @@ cudaError_t launch_after(void (*kernel)(P...), int grid, int block, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
-// (A block of 32 x 32 entries of a row-major matrix, as a warp stores it: 64-byte
-// rows in the 64-byte swizzle.)
-inline bool make_store_map(CUtensorMap *map, void *base, bool bf16, long cols, long rows,
-                           long pitch) {
+// A row-major output that warps store (or add to) in blocks of 32 rows of 64 bytes,
+// in the 64-byte swizzle; `layers` matrices of `rows` rows in turn.
+inline bool make_store_map(CUtensorMap *map, void *base, CUtensorMapDataType type, int bytes,
+                           long cols, long rows, long pitch, int layers = 1) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
-  cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)pitch * 2 * (cuuint64_t)rows};
-  cuuint32_t box[3] = {32, 32, 1};
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)layers};
+  cuuint64_t strides[2] = {(cuuint64_t)pitch * bytes, (cuuint64_t)pitch * bytes * (cuuint64_t)rows};
+  cuuint32_t box[3] = {(cuuint32_t)(64 / bytes), 32, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base,
-            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return fn(map, type, 3, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Sets a kernel's shared memory, and checks that the block is launched with at

@@ -314,6 +314,33 @@ struct StatsEpi {
   __device__ __forceinline__ void finish() {}
 };
 
+// A warp's block of 32 rows of 64 bytes (16 x 4 bytes a lane, its row) leaves by TMA
+// to (col, row0, layer), stored or added; two blocks of the scratch memory take turns.
+__device__ __forceinline__ void send_block(const CUtensorMap *map, uint8_t *scratch, int turn,
+                                           const uint4 (&v)[4], int col, int row0, int layer,
+                                           bool add) {
+  const int lane = threadIdx.x & 31;
+  uint8_t *block = scratch + (turn & 1) * 2048;
+  if (lane == 0) bulk_wait_read<1>();  // the block before the last has left
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 4; q++)
+    *reinterpret_cast<uint4 *>(block + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) = v[q];
+  fence_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (add)
+      tma_add_3d(map, block, col, row0, layer);
+    else
+      tma_store_3d(map, block, col, row0, layer);
+    bulk_commit();
+  }
+}
+__device__ __forceinline__ void blocks_sent() {
+  if ((threadIdx.x & 31) == 0) bulk_wait_all();
+  __syncwarp();
+}
+
 // Backward: D of one piece (columns v0 .. v0 + v) in the operands' type.  Its
 // rounding is that of one operand of a product whose sums are FP32, as H's and
 // W's own roundings are.  Rows and columns past the ends are zeros: they are
@@ -322,20 +349,13 @@ template <bool BF16>
 struct GradEpi {
   const int *label;
   const float *lse, *grad, *scale;
-  uint16_t *d;
-  long pitch;     // multiple of 256
   int v0, v;
 
   __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, bool, bool, int m,
-                                       const CUtensorMap *, uint8_t *, int *) {
+                                       const CUtensorMap *mapD, uint8_t *scratch, int *) {
     const int row0 = row - (int)(threadIdx.x & 31);
-    uint4 *dst = reinterpret_cast<uint4 *>(d + (size_t)row * pitch + col0);
-    if (row0 >= m) {  // no row of this warp: zeros, as far as the last stage of D^T H reads
-      if (row0 < (m + kStageK - 1) / kStageK * kStageK)
-#pragma unroll
-        for (int q = 0; q < 16; q++) dst[q] = make_uint4(0, 0, 0, 0);
-      return;
-    }
+    // no row of this warp: zeros, as far as the last stage of D^T H reads
+    if (row0 >= (m + kStageK - 1) / kStageK * kStageK) return;
     const bool in = row < m;
     const int y = in ? label[row] - v0 - col0 : -1;
     // 2^E p = 2^(z log2 e - lse log2 e + E), so that p's own range does not cut it
@@ -360,15 +380,17 @@ struct GradEpi {
       }
 #pragma unroll
       for (int i = 0; i < 32; i++) x[i] = (in && i < left) ? x[i] * gr : 0.f;
+      uint4 o[4];
 #pragma unroll
       for (int q = 0; q < 4; q++)
-        dst[g * 4 + q] = make_uint4(pack2<BF16>(x[8 * q], x[8 * q + 1]),
-                                    pack2<BF16>(x[8 * q + 2], x[8 * q + 3]),
-                                    pack2<BF16>(x[8 * q + 4], x[8 * q + 5]),
-                                    pack2<BF16>(x[8 * q + 6], x[8 * q + 7]));
+        o[q] = make_uint4(pack2<BF16>(x[8 * q], x[8 * q + 1]),
+                          pack2<BF16>(x[8 * q + 2], x[8 * q + 3]),
+                          pack2<BF16>(x[8 * q + 4], x[8 * q + 5]),
+                          pack2<BF16>(x[8 * q + 6], x[8 * q + 7]));
+      send_block(mapD, scratch, g, o, col0 + g * 32, row0, 0, false);
     }
   }
-  __device__ __forceinline__ void finish() {}
+  __device__ __forceinline__ void finish() { blocks_sent(); }
 };
 
 // dW, and dH where it comes out of one product: scaled back, rounded once, to the
@@ -411,18 +433,8 @@ struct StoreEpi {
         v[q] = make_uint4(w[0], w[1], w[2], w[3]);
       }
       if constexpr (TMA) {
-        uint8_t *block = scratch + (g & 1) * 2048;
-        if (lane == 0) bulk_wait_read<1>();  // the block before the last has left
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < 4; q++)
-          *reinterpret_cast<uint4 *>(block + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) = v[q];
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(mapD, block, col0 + g * 32, row0, 0);  // rows from m on are cut off by the map
-          bulk_commit();
-        }
+        // (rows from m on are cut off by the map)
+        send_block(mapD, scratch, g, v, col0 + g * 32, row0, 0, false);
       } else {
 #pragma unroll
         for (int q = 0; q < 4; q++) *reinterpret_cast<uint4 *>(scratch + lane * 80 + q * 16) = v[q];
@@ -449,8 +461,7 @@ struct StoreEpi {
     }
   }
   __device__ __forceinline__ void finish() {
-    if (TMA && (threadIdx.x & 31) == 0) bulk_wait_all();
-    __syncwarp();
+    if (TMA) blocks_sent();
   }
 };
 
@@ -464,7 +475,7 @@ struct SumEpi {
 
   __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int split, bool, bool,
                                        int m, const CUtensorMap *mapD, uint8_t *scratch, int *) {
-    const int lane = threadIdx.x & 31, row0 = row - lane;
+    const int row0 = row - (int)(threadIdx.x & 31);
     if (row0 >= m) return;  // no row of this warp (rows past m within it: sums that nothing reads)
 #pragma unroll 1
     for (int g = 0; g < 8; g++) {
@@ -472,28 +483,13 @@ struct SumEpi {
       __syncwarp();
       tmem_ld16(taddr + g * 16, r);
       tmem_wait_ld();
-      uint8_t *block = scratch + (g & 1) * 2048;
-      if (lane == 0) bulk_wait_read<1>();  // the block before the last has left
-      __syncwarp();
-#pragma unroll
-      for (int q = 0; q < 4; q++)
-        *reinterpret_cast<uint4 *>(block + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) =
-            make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        if (add)
-          tma_add_3d(mapD, block, col0 + g * 16, row0, split);
-        else
-          tma_store_3d(mapD, block, col0 + g * 16, row0, split);
-        bulk_commit();
-      }
+      const uint4 v[4] = {make_uint4(r[0], r[1], r[2], r[3]), make_uint4(r[4], r[5], r[6], r[7]),
+                          make_uint4(r[8], r[9], r[10], r[11]),
+                          make_uint4(r[12], r[13], r[14], r[15])};
+      send_block(mapD, scratch, g, v, col0 + g * 16, row0, split, add);
     }
   }
-  __device__ __forceinline__ void finish() {
-    if ((threadIdx.x & 31) == 0) bulk_wait_all();
-    __syncwarp();
-  }
+  __device__ __forceinline__ void finish() { blocks_sent(); }
 };
 
 // dH from those sums, the parts in their order: four columns a thread, eight parts
@@ -714,9 +710,14 @@ cudaError_t backward(Prep p, const uint16_t *W, long ldw, uint16_t *dW, long ldd
   uint16_t *d = at<uint16_t>(ws, L.d);
   float *acc = at<float>(ws, L.acc);
   const long acc_pitch = (long)os2_round_up((size_t)p.k, 256);
-  CUtensorMap mh, mht, mw, mwt, md, mdt, msum;
+  CUtensorMap mh, mht, mw, mwt, md, mdt, mds, msum;
+  const CUtensorMapDataType type =
+      BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   if (!make_map(&mh, p.Hc, BF16, p.k, p.n, L.kp, false) ||
-      !make_map(&mht, p.Hc, BF16, p.k, L.npad, L.kp, true))
+      !make_map(&mht, p.Hc, BF16, p.k, L.npad, L.kp, true) ||
+      !make_map(&md, d, BF16, L.vc, L.npad, L.vc, false) ||
+      !make_map(&mdt, d, BF16, L.vc, L.npad, L.vc, true) ||
+      !make_store_map(&mds, d, type, 2, L.vc, L.npad, L.vc))
     return cudaErrorInvalidValue;
   const bool sums = L.pieces * L.splits > 1;
   if (p.dH && sums &&
@@ -727,13 +728,11 @@ cudaError_t backward(Prep p, const uint16_t *W, long ldw, uint16_t *dW, long ldd
     const int v0 = i * L.vc, vn = std::min(L.vc, p.v - v0);
     const uint16_t *Wi = W + (size_t)v0 * ldw;
     if (!make_map(&mw, Wi, BF16, p.k, vn, ldw, false) ||
-        !make_map(&mwt, Wi, BF16, p.k, vn, ldw, true) ||
-        !make_map(&md, d, BF16, L.vc, L.npad, L.vc, false) ||
-        !make_map(&mdt, d, BF16, L.vc, L.npad, L.vc, true))
+        !make_map(&mwt, Wi, BF16, p.k, vn, ldw, true))
       return cudaErrorInvalidValue;
-    const GradEpi<BF16> ge{p.label, p.lse_c, p.grad_c, p.scale, d, L.vc, v0, vn};
+    const GradEpi<BF16> ge{p.label, p.lse_c, p.grad_c, p.scale, v0, vn};
     e = launch_mm2<BF16, false, false>(mh, mw, Job{p.n, vn, p.k, p.count, nullptr, INT_MAX, 1}, ge,
-                                       p.status, s);
+                                       p.status, s, &mds);
     if (e != cudaSuccess) return e;
     if (p.dH) {
       // (a shorter last piece may have fewer stages than parts: those add nothing)
@@ -753,9 +752,7 @@ cudaError_t backward(Prep p, const uint16_t *W, long ldw, uint16_t *dW, long ldd
       const Job job{vn, p.k, p.n, nullptr, p.count, INT_MAX, 1, p.dH != nullptr};
       if (tma_rows(dW, lddw)) {
         CUtensorMap mo;
-        if (!make_store_map(&mo, out,
-                            BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                            2, p.k, vn, lddw)) return cudaErrorInvalidValue;
+        if (!make_store_map(&mo, out, type, 2, p.k, vn, lddw)) return cudaErrorInvalidValue;
         e = launch_mm2<BF16, true, true>(
             mdt, mht, job, StoreEpi<BF16, true>{out, lddw, nullptr, p.scale, vn, p.k, true}, p.status,
             s, &mo);

@@ -472,7 +472,7 @@ os2_status os2_xent_backward(int n, int k, int v, int dtype, const void *H, int 
  *   m = a sgn(c) (|c| / 127)^2,   v = a (c / 255)^4,
  * re-encoded to the nearest code (of the square and fourth root) after the
  * update, positive v to code 1 at least.  Codes and scales of zero are the
- * initial state.  In the quotient, v / (1 - beta2^step) below 2^-126 counts as 0.
+ * initial state.  In the quotient, v / (1 - beta2^step) and eps below 2^-126 count as 0.
  * A non-finite gradient makes its element (32-bit) or its block
  * (8-bit) non-finite, as the formula does.  Tensors whose pointers are all
  * 16-byte aligned are fastest. */

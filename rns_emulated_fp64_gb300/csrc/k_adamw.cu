@@ -15,7 +15,7 @@
 // with FP32 parameters, gradients and moments.  A warp takes 256 elements (an 8-bit
 // block), a lane 8 consecutive ones, all loads before the arithmetic: more than 100
 // KB an SM in flight with FP32 moments.  With 8-bit ones the bytes are fewer and
-// the arithmetic (some 50 instructions an element) weighs as much as they do: six
+// the arithmetic (some 75 instructions an element) weighs as much as they do: six
 // CTAs an SM rather than five are worth 6 %, conversions are additions of 2^23 and
 // 1.5 2^23 instead of I2F and F2I, which run at a quarter of the rate, and the
 // exact rounding is taken only where the fast one is in doubt.
@@ -122,8 +122,10 @@ __device__ __forceinline__ float m_value(float c, float a) {
   const float t = __fmul_rn(c, 1.0f / 127.0f);
   return __fmul_rn(a, __fmul_rn(t, fabsf(t)));
 }
-__device__ __forceinline__ float v_value(float c, float a) {
-  float t = __fmul_rn(c, 1.0f / 255.0f);
+// x: 2^23 + c; the product c / 255 in one step, exactly as if c were multiplied
+// (2^23 times the constant is a shift of it).
+__device__ __forceinline__ float v_value(float x, float a) {
+  float t = __fmaf_rn(x, 1.0f / 255.0f, -8388608.0f * (1.0f / 255.0f));
   t = __fmul_rn(t, t);
   return __fmul_rn(a, __fmul_rn(t, t));
 }
@@ -142,12 +144,11 @@ __device__ __forceinline__ void m_values(uint32_t lo, uint32_t hi, float a, floa
 #undef M4
 }
 __device__ __forceinline__ void v_values(uint32_t lo, uint32_t hi, float a, float (&x)[8]) {
-  constexpr float less = 8388608.0f;
-#define V4(w, o)                                                                      \
-  x[o] = v_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)) - less, a);     \
-  x[o + 1] = v_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441)) - less, a); \
-  x[o + 2] = v_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)) - less, a); \
-  x[o + 3] = v_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443)) - less, a);
+#define V4(w, o)                                                               \
+  x[o] = v_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)), a);     \
+  x[o + 1] = v_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441)), a); \
+  x[o + 2] = v_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)), a); \
+  x[o + 3] = v_value(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443)), a);
   V4(lo, 0)
   V4(hi, 4)
 #undef V4
@@ -156,15 +157,21 @@ __device__ __forceinline__ void v_values(uint32_t lo, uint32_t hi, float a, floa
 // The nearest code of m / a, of v / a (a > 0): rint(127 sqrt(|m| / a)) and
 // rint(255 sqrt(sqrt(v / a))), every operation correctly rounded.  Those take some
 // 60 instructions an element and would bound the kernel, so the approximate
-// instructions decide first: with 1 / a, the products and the roots each within
-// 2^-23, 127 times the root is off by less than 4e-5 and 255 times the fourth root
-// by less than 1e-4.  Only where one of them lies nearer than 6e-5 or 1.5e-4 to a
-// tie (one element in 2000) both take the exact way.  The limits are negative,
-// for every element to take it, where 1 / a or the quotients could leave the
-// normal numbers.  A code is the low byte of its FP32 value plus 1.5 2^23.
+// instructions decide first, with 127^2 / a and 255^4 / a as factors and roots within
+// 2^-23: the root is off by less than 2.7e-5 and the fourth root by less than 6.1e-5,
+// the correctly rounded ones themselves by less than 2e-5 and 4.2e-5.  Only where one
+// lies nearer than 6e-5 or 1.5e-4 to a tie (one element in 2000) both take the exact
+// way, asked for once every four elements.  The limits are negative, for every
+// element to take it, where the factors or the quotients could leave the normal
+// numbers.  A code is the low byte of its FP32 value plus 1.5 2^23.
 __device__ __forceinline__ float sqrt_fast(float x) {
   float y;
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 constexpr float kRound = 12582912.0f;  // 1.5 * 2^23
@@ -177,36 +184,49 @@ __device__ __forceinline__ Encode encode_with(float am, float av) {
   Encode e;
   e.am = am;
   e.av = av;
-  const bool fm = am > 1e-30f && am < 1e30f, fv = av > 1e-30f && av < 1e30f;
-  e.rm = fm ? __frcp_rn(am) : 0.f;
-  e.rv = fv ? __frcp_rn(av) : 0.f;
+  const bool fm = am > 1e-26f && am < 1e30f, fv = av > 1e-26f && av < 1e30f;
+  e.rm = fm ? __fmul_rn(__frcp_rn(am), 127.0f * 127.0f) : 0.f;
+  e.rv = fv ? __fmul_rn(__frcp_rn(av), 255.0f * 255.0f * 255.0f * 255.0f) : 0.f;
   // a block of zeros: every code is 0 without a division by 0
   e.dm = fm ? 0.5f - 6e-5f : am > 0.f ? -1.f : 1.f;
   e.dv = fv ? 0.5f - 1.5e-4f : av > 0.f ? -1.f : 1.f;
   return e;
 }
-// Codes in the low bytes of cm and cv.
-__device__ __forceinline__ void codes(const Encode &e, float m, float v, uint32_t &cm,
-                                      uint32_t &cv) {
-  const float x = sqrt_fast(fabsf(m) * e.rm) * 127.0f;
-  const float y = sqrt_fast(sqrt_fast(v * e.rv)) * 255.0f;
-  float p = x + kRound, q = y + kRound;
-  // NaN too (a block that holds Inf or NaN has such a scale: whatever its codes, its
-  // values are not numbers)
-  if (!(fabsf(x - (p - kRound)) <= e.dm) || !(fabsf(y - (q - kRound)) <= e.dv)) {
-    if (e.am > 0.f) p = rintf(__fmul_rn(__fsqrt_rn(__fdiv_rn(fabsf(m), e.am)), 127.0f)) + kRound;
-    if (e.av > 0.f)
-      q = rintf(__fmul_rn(__fsqrt_rn(__fsqrt_rn(__fdiv_rn(v, e.av))), 255.0f)) + kRound;
+// Codes of four moments in the low bytes of cm and cv: the sum of a negative number
+// and 1.5 2^23 ends in its two's complement.
+__device__ __forceinline__ void codes(const Encode &e, const float *m, const float *v,
+                                      uint32_t (&cm)[4], uint32_t (&cv)[4]) {
+  float off_m = 0.f, off_v = 0.f;  // furthest from the rounded value
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const float x = copysignf(sqrt_fast(fabsf(m[i]) * e.rm), m[i]);
+    const float y = sqrt_fast(sqrt_fast(v[i] * e.rv));
+    const float p = x + kRound, q = y + kRound;
+    off_m = fmaxf(off_m, fabsf(x - (p - kRound)));
+    off_v = fmaxf(off_v, fabsf(y - (q - kRound)));
+    cm[i] = __float_as_uint(p);
+    cv[i] = __float_as_uint(q);
   }
-  const uint32_t c = __float_as_uint(p);
-  cm = m < 0.f ? 0u - c : c;
-  cv = max(__float_as_uint(q), 0x4B400000u + (v > 0.f ? 1u : 0u));
-}
-
-// The largest magnitude by its bits, which order as the values do and put Inf and
-// NaN above every number.
-__device__ __forceinline__ void larger(uint32_t &top, float x) {
-  top = max(top, __float_as_uint(x) & 0x7FFFFFFFu);
+  // (where the block holds Inf or NaN its limits are negative: whatever its codes, its
+  // values are not numbers)
+  if (off_m > e.dm || off_v > e.dv) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const float x = sqrt_fast(fabsf(m[i]) * e.rm), y = sqrt_fast(sqrt_fast(v[i] * e.rv));
+      if (fabsf(x - rintf(x)) > e.dm || fabsf(y - rintf(y)) > e.dv) {
+        if (e.am > 0.f)
+          cm[i] = __float_as_uint(
+              copysignf(rintf(__fmul_rn(__fsqrt_rn(__fdiv_rn(fabsf(m[i]), e.am)), 127.0f)), m[i]) +
+              kRound);
+        if (e.av > 0.f)
+          cv[i] = __float_as_uint(
+              rintf(__fmul_rn(__fsqrt_rn(__fsqrt_rn(__fdiv_rn(v[i], e.av))), 255.0f)) + kRound);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; i++)  // a positive v never becomes 0
+    cv[i] = __viaddmax_u32(min(__float_as_uint(v[i]), 1u), 0x4B400000u, cv[i]);
 }
 
 template <int PT, int GT, bool Q8>
@@ -256,10 +276,10 @@ __global__ void __launch_bounds__(kThreads, Q8 ? 6 : 1) k_adamw(const __grid_con
     m[i] = __fadd_rn(__fmul_rn(m[i], st.b1), __fmul_rn(g, st.one_b1));
     v[i] = __fadd_rn(__fmul_rn(v[i], st.b2), __fmul_rn(__fmul_rn(g, g), st.one_b2));
     const float d = sqrt_fast(v[i] * st.c2) + st.eps;  // 2^-22 of the update
-    p8[i] = Elem<PT>::put(Elem<PT>::get(p8[i]) * st.decay - __fdividef(m[i] * st.lr_c1, d));
-    if (Q8) {
-      larger(am, m[i]);
-      larger(av, v[i]);
+    p8[i] = Elem<PT>::put(Elem<PT>::get(p8[i]) * st.decay - m[i] * st.lr_c1 * rcp_fast(d));
+    if (Q8 && (i & 1)) {  // by their bits, which put Inf and NaN above every number (v >= 0)
+      am = __vimax3_u32(am, __float_as_uint(m[i - 1]) & 0x7FFFFFFFu, __float_as_uint(m[i]) & 0x7FFFFFFFu);
+      av = __vimax3_u32(av, __float_as_uint(v[i - 1]), __float_as_uint(v[i]));
     }
   }
   store8(pp, p8, n, vec);
@@ -276,8 +296,7 @@ __global__ void __launch_bounds__(kThreads, Q8 ? 6 : 1) k_adamw(const __grid_con
 #pragma unroll
     for (int h = 0; h < 2; h++) {
       uint32_t x[4], y[4];
-#pragma unroll
-      for (int i = 0; i < 4; i++) codes(e, m[4 * h + i], v[4 * h + i], x[i], y[i]);
+      codes(e, m + 4 * h, v + 4 * h, x, y);
       cm.w[h] = __byte_perm(__byte_perm(x[0], x[1], 0x0040), __byte_perm(x[2], x[3], 0x0040), 0x5410);
       cv.w[h] = __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
     }

@@ -2,8 +2,9 @@
 //
 // A CTA streams its share of the weights through a ring of TMA copies (up to 200
 // KB an SM in flight, whatever the registers hold) with the tokens' matching
-// terms beside them.  Eight warps take 16 channels each of a stage of 128
-// channels x 128 terms: a lane reads 16 bytes of two channels at a time, widens
+// terms beside them.  Eight warps take 16 channels each of a stage of 128 channels
+// x 128 terms (up to 16 tokens, two groups of eight the stages in turn: the group that
+// works reads shared memory while the other multiplies): a lane reads 16 bytes of two channels at a time, widens
 // them to FP16 in registers (exact) and multiplies with mma.sync.m16n8k16, whose
 // fragments are the lanes' own bytes: the 16 terms of an instruction may be any,
 // as long as the tokens' are the same, so lane t's 16 consecutive bytes serve four
@@ -18,24 +19,35 @@
 // through global memory, with stages dealt out evenly over single CTAs, took 3 us
 // longer: 12.5 us instead of 8 for 4096 x 4096 and one token.)
 //
-// Warps (9): 0-7 as above, 8 TMA.  The first weights are asked for before the kernel waits
-// for the one in front of it on the stream, which quantises the tokens: they are
-// inputs of the call, and nothing in front of that kernel can be writing them
-// still.  Every wait is bounded, as in mm2.cuh.
+// Warps: 8 or 16 as above, one more for TMA.  The first weights are asked for before
+// the kernel waits for the one in front of it on the stream, which quantises the
+// tokens: they are inputs of the call, and nothing in front of that kernel can be
+// writing them still.  Every wait is bounded, as in mm2.cuh.
+//
+// Measured with the quantising launch: one token 8.3 us for 4096 x 4096 weights, 17.3
+// for 14336 x 4096 and 17.9 for 32000 x 2048 (3.7 TB/s; a kernel that only reads takes 6.2, 12.4
+// and 13.6); 12 tokens 9.3, 18.5 and 19.6.  The rest is the start of the ring, 500 cycles
+// of shared memory a stage (weights in and out, tokens) against 740 of DRAM, and tiles
+// that do not divide by the SMs.
 #include "i8.cuh"
 
 using namespace os2i8;
 
 namespace {
 
-constexpr int kFewWarps = 8, kFewThreads = 32 * kFewWarps + 32;
+constexpr int kFewWarps = 8;                     // of a group, 16 channels each
 constexpr uint32_t kFewW = 128 * kStageK;        // a stage's weights
 
 template <int NG>
 struct Few {
+  // Up to 16 tokens, two groups of warps take the stages in turn: 17.9 us against 19.1
+  // for one token and 32000 x 2048 weights, 8.3 against 8.8 for 4096 x 4096; above,
+  // their exchange costs more than it gives (25.1 against 24.2 for 32 tokens).
+  static constexpr int groups = NG <= 2 ? 2 : 1;
+  static constexpr int all = kFewWarps * groups, threads = 32 * all + 32;
   static constexpr uint32_t block = NG * 8 * kBK * 2;        // one k-block of the tokens
   static constexpr uint32_t stage = kFewW + 2 * block;
-  static constexpr uint32_t part = kFewWarps * NG * 32 * 16;  // a tile's sums, one side
+  static constexpr uint32_t part = all * NG * 32 * 16;  // a tile's sums, one side
   static constexpr int stages = (int)((227 * 1024 - 1024 - 512 - 2 * part) / stage);
   static constexpr size_t smem = 1024 + (size_t)stages * stage + 2 * part + 512;
 };
@@ -58,7 +70,7 @@ struct FewJob {
 };
 
 template <int NG>
-__global__ void __launch_bounds__(kFewThreads, 1)
+__global__ void __launch_bounds__(Few<NG>::threads, 1)
     k_i8few(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapT,
             const FewJob j, int *status) {
   using F = Few<NG>;
@@ -77,7 +89,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < F::stages; s++) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kFewWarps);
+      mbar_init(&empty[s], kFewWarps);  // of the group that takes it
     }
     for (int s = 0; s < 2 * kFewWarps; s++) mbar_init(&part[s], 1);
     *s_abort = 0;
@@ -94,7 +106,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     return false;
   };
 
-  if (warp == kFewWarps) {
+  if (warp == F::all) {
     // ------------------------------------------------------------ TMA
     if (lane == 0) {
       auto weights = [&](int st, int tc, int ks) {
@@ -144,16 +156,20 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   } else {
     // ------------------------------------------------------------ products
     const int g = lane >> 2, t4 = lane & 3;
-    // 16-byte piece c of a 128-byte row r of a swizzled block: c ^ (r & 7), and r & 7 == g
-    const uint32_t w0 = (uint32_t)(warp * 16 + g) * 128, w1 = w0 + 8 * 128;
-    int st = 0;
+    // 16-byte piece c of a 128-byte row r of a swizzled block: c ^ (r & 7).  Lane row g
+    // takes row gw of the eight: then eight lanes that read at once have two rows four
+    // apart, whose pieces are in different banks (two neighbours' are in the same).
+    const int gw = g >> 1 | (g & 1) << 2;
+    const int group = warp / kFewWarps, cw = warp % kFewWarps;
+    const uint32_t w0 = (uint32_t)(cw * 16 + gw) * 128, w1 = w0 + 8 * 128;
+    int st = 0, turn = 0;
     uint32_t ph = 0;
     // Entry (q, e) of a thread: channel ch + 8 (e / 2), token 8 q + 2 t4 + e % 2.  The
-    // channels of lane row g meet in CTA g C / 8 of the cluster.  A warp sends the
-    // sums of tile i + 2 after it has had everyone's of tile i + 1, which their warps
+    // channels of lane row g meet in CTA g C / 8 of the cluster, in group 0.  A warp
+    // sends the sums of tile i + 2 after it has had everyone's of tile i + 1, which their warps
     // sent after they had read tile i: two sides are enough.
     const int owner = g * j.cluster / 8;
-    const bool mine = owner == rank;
+    const bool mine = owner == rank && group == 0;
     bool waited = false;  // for the kernel in front, and for the cluster
     bool ok = true;
     int side = 0;
@@ -165,7 +181,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       for (int q = 0; q < NG; q++)
 #pragma unroll
         for (int e = 0; e < 4; e++) acc[q][e] = 0.f, sum[q][e] = 0;
-      const int ch = t * 128 + warp * 16 + g;
+      const int ch = t * 128 + cw * 16 + gw;
       float sb[2], bias[2];
 #pragma unroll
       for (int h = 0; h < 2; h++) {
@@ -173,13 +189,23 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         sb[h] = in ? j.sb[ch + 8 * h] : 0.f;
         bias[h] = in && j.bias ? j.bias[ch + 8 * h] : 0.f;
       }
+      int held = 0;  // stages in acc
       for (int ks = s0; ks < s1; ks++) {
+        if (turn != group) {
+          turn = (turn + 1) % F::groups;
+          if (++st == F::stages) {
+            st = 0;
+            ph ^= 1;
+          }
+          continue;
+        }
+        turn = (turn + 1) % F::groups;
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[st], ph, s_abort, kWaitLimit));
         if (!ok) break;
         const uint32_t base = smem_u32(smem + st * F::stage);
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-          const uint32_t at = (uint32_t)((4 * h + t4) ^ g) << 4;
+          const uint32_t at = (uint32_t)((4 * h + t4) ^ gw) << 4;
           const uint4 a = lds16(base + w0 + at), b = lds16(base + w1 + at);
           uint4 x[NG][2];
 #pragma unroll
@@ -207,49 +233,58 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           st = 0;
           ph ^= 1;
         }
-        if ((ks - s0) % 8 == 7 || ks == s1 - 1) {
+        if (++held == 8) {
+          held = 0;
 #pragma unroll
           for (int q = 0; q < NG; q++)
 #pragma unroll
             for (int e = 0; e < 4; e++) sum[q][e] += __float2int_rn(acc[q][e]), acc[q][e] = 0.f;
         }
       }
+#pragma unroll
+      for (int q = 0; q < NG; q++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) sum[q][e] += __float2int_rn(acc[q][e]);
       if (!ok) break;
       if (!waited) {  // the tokens' scales and the output; the other CTAs' barriers
         wait_for_previous();
         cluster_wait();
         waited = true;
       }
-      if (j.cluster > 1) {
-        // the parts of a channel's C CTAs lie side by side: [C][8 / C lane rows] lanes
-        const uint32_t bar = smem_u32(&part[side * kFewWarps + warp]);
-        const uint32_t buf = smem_u32(sPart + side * F::part);
+      if (j.cluster * F::groups > 1) {
+        // the parts of a channel's C CTAs and their groups lie side by side:
+        // [C][groups][8 / C lane rows] lanes
+        const uint32_t bar = smem_u32(&part[side * kFewWarps + cw]);
+        const uint32_t buf = smem_u32(sPart + side * F::part) + (uint32_t)cw * NG * 512 * F::groups;
         const int per = 32 / j.cluster;  // lanes of a part
-        const uint32_t to = mapa_shared(buf, owner) + (uint32_t)warp * NG * 512 +
-                            (uint32_t)(rank * per + (lane & (per - 1))) * 16;
+        const uint32_t to = mapa_shared(buf, owner) +
+                            (uint32_t)((rank * F::groups + group) * per + (lane & (per - 1))) * 16;
         const uint32_t to_bar = mapa_shared(bar, owner);
-        if (lane == 0) mbar_arrive_expect_tx(&part[side * kFewWarps + warp], NG * 512);
+        if (lane == 0 && group == 0)
+          mbar_arrive_expect_tx(&part[side * kFewWarps + cw], NG * 512 * F::groups);
 #pragma unroll
         for (int q = 0; q < NG; q++)
-          st_async16(to + q * 512, to_bar, sum[q][0], sum[q][1], sum[q][2], sum[q][3]);
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&part[side * kFewWarps + warp], pph, s_abort,
-                                                       kWaitLimit));
+          st_async16(to + q * 512 * F::groups, to_bar, sum[q][0], sum[q][1], sum[q][2], sum[q][3]);
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_bounded(&part[side * kFewWarps + cw], pph, s_abort, kWaitLimit));
         if (!ok) break;
-        const uint32_t from = buf + (uint32_t)warp * NG * 512 + (uint32_t)(lane & (per - 1)) * 16;
+        if (mine) {
+          const uint32_t from = buf + (uint32_t)(lane & (per - 1)) * 16;
 #pragma unroll
-        for (int q = 0; q < NG; q++) {
-          int4 v = make_int4(0, 0, 0, 0);
-          for (int p = 0; p < j.cluster; p++) {
-            const uint4 x = lds16(from + q * 512 + (uint32_t)(p * per) * 16);
-            v.x += (int)x.x;
-            v.y += (int)x.y;
-            v.z += (int)x.z;
-            v.w += (int)x.w;
+          for (int q = 0; q < NG; q++) {
+            int4 v = make_int4(0, 0, 0, 0);
+            for (int p = 0; p < j.cluster * F::groups; p++) {
+              const uint4 x = lds16(from + q * 512 * F::groups + (uint32_t)(p * per) * 16);
+              v.x += (int)x.x;
+              v.y += (int)x.y;
+              v.z += (int)x.z;
+              v.w += (int)x.w;
+            }
+            sum[q][0] = v.x;
+            sum[q][1] = v.y;
+            sum[q][2] = v.z;
+            sum[q][3] = v.w;
           }
-          sum[q][0] = v.x;
-          sum[q][1] = v.y;
-          sum[q][2] = v.z;
-          sum[q][3] = v.w;
         }
         side ^= 1;
         if (side == 0) pph ^= 1;
@@ -289,7 +324,7 @@ cudaError_t launch(const I8Args &a, cudaStream_t s) {
   j.n = a.n;
   j.tiles = (a.n + 127) / 128;
   j.stages = (a.k + kStageK - 1) / kStageK;
-  few_clusters(reinterpret_cast<const void *>(k_i8few<NG>), kFewThreads, F::smem, j.tiles, j.stages,
+  few_clusters(reinterpret_cast<const void *>(k_i8few<NG>), F::threads, F::smem, j.tiles, j.stages,
                &j.cluster, &j.clusters);
   CUtensorMap mw, mt;
   if (!map_w(&mw, a.W, a.k, a.n, a.ldw) ||
@@ -301,7 +336,7 @@ cudaError_t launch(const I8Args &a, cudaStream_t s) {
   j.bias = a.bias;
   j.y = a.y;
   j.ldy = a.ldy;
-  return launch_cluster(k_i8few<NG>, j.cluster, j.cluster * j.clusters, kFewThreads, F::smem,
+  return launch_cluster(k_i8few<NG>, j.cluster, j.cluster * j.clusters, F::threads, F::smem,
                         a.overlap, s, mw, mt, j, a.status);
 }
 

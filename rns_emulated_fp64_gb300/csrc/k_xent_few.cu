@@ -139,8 +139,10 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
   } else {
     // ------------------------------------------------------------ products
     const int g = lane >> 2, t4 = lane & 3;
-    const uint32_t w0 = (uint32_t)(warp * 16 + g) * 128, w1 = w0 + 8 * 128;
-    // Entry (q, e): row ch + 8 (e / 2) of W, packed row 8 q + 2 t4 + e % 2 of H.  Rows of
+    // Lane row g takes row gw of eight, of W and of H: no bank conflicts (k_i8few.cu).
+    const int gw = g >> 1 | (g & 1) << 2;
+    const uint32_t w0 = (uint32_t)(warp * 16 + gw) * 128, w1 = w0 + 8 * 128;
+    // Entry (q, e): row ch + 8 (e / 2) of W, packed row 8 q + t4 + 4 (e % 2) of H.  Rows of
     // lane row g meet in CTA g C / 8; two sides are enough (k_i8few.cu).
     const int owner = g * j.cluster / 8;
     const bool mine = owner == rank;
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
     for (int q = 0; q < NG; q++)
 #pragma unroll
       for (int e = 0; e < 2; e++) {
-        const int r = q * 8 + 2 * t4 + e;
+        const int r = q * 8 + t4 + 4 * e;
         label[q][e] = r < m ? j.label[r] : -1;
         top[q][e] = -INFINITY;
         total[q][e] = 0.f;
@@ -173,11 +175,11 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
         const uint32_t base = smem_u32(smem + st * S::stage);
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-          const uint32_t at = (uint32_t)((4 * h + t4) ^ g) << 4;  // 8 terms of rows g, g + 8
+          const uint32_t at = (uint32_t)((4 * h + t4) ^ gw) << 4;  // 8 terms
           const uint4 a = lds16(base + w0 + at), b = lds16(base + w1 + at);
 #pragma unroll
           for (int q = 0; q < NG; q++) {
-            const uint4 x = lds16(base + kW + (uint32_t)(q * 8 + g) * 128 + at);
+            const uint4 x = lds16(base + kW + (uint32_t)(q * 8 + gw) * 128 + at);
             mma<BF16>(acc[q], a.x, b.x, a.y, b.y, x.x, x.y);
             mma<BF16>(acc[q], a.z, b.z, a.w, b.w, x.z, x.w);
           }
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
       if (mine)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-          const int ch = t * 128 + warp * 16 + g;
+          const int ch = t * 128 + warp * 16 + gw;
 #pragma unroll
           for (int q = 0; q < NG; q++)
 #pragma unroll
@@ -238,7 +240,7 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
               const float z = sum[q][2 * h + e];
               if (ch + 8 * h < j.v) {
                 add_exp(top[q][e], total[q][e], z * kLog2e, 1.f);
-                if (ch + 8 * h == label[q][e]) j.zlabel[q * 8 + 2 * t4 + e] = z;
+                if (ch + 8 * h == label[q][e]) j.zlabel[q * 8 + t4 + 4 * e] = z;
               }
             }
         }
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
           const float y = __shfl_xor_sync(0xffffffffu, total[q][e], o);
           add_exp(top[q][e], total[q][e], x, y);
         }
-        if (g == 0) stats[warp * NG * 8 + q * 8 + 2 * t4 + e] = make_float2(top[q][e], total[q][e]);
+        if (g == 0) stats[warp * NG * 8 + q * 8 + t4 + 4 * e] = make_float2(top[q][e], total[q][e]);
       }
   }
   // the pairs are written; and no CTA leaves while another may still send to it

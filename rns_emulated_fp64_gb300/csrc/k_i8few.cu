@@ -119,10 +119,16 @@ __global__ void __launch_bounds__(Few<NG>::threads, 1)
           tma_load_3d(smem + st * F::stage + kFewW + h * F::block, &mapT, &full[st],
                       ks * kStageK + h * kBK, 0, 0);
       };
-      // the first turn of the ring: weights, then, once they are there, tokens
+      // The first weights; then, once they are there, the tokens with the rest.  A long
+      // stream does not ask for the whole ring at first: memory serves all that is asked for
+      // side by side, so the first stage would be there as late as the last, and the
+      // tokens behind it (32000 x 2048, one token: 18.0 us with the whole ring, 16.7 with
+      // 6 stages; a CTA that has its whole share in the ring: 8.5 with all 8 of them, 8.8 with 6).
+      const int share = (j.tiles - first + j.clusters - 1) / j.clusters * (s1 - s0);
+      const int ahead = share <= F::stages ? F::stages : min(6, F::stages);
       int i = 0;
-      for (int t = first; t < j.tiles && i < F::stages; t += j.clusters)
-        for (int ks = s0; ks < s1 && i < F::stages; ks++) weights(i++, t, ks);
+      for (int t = first; t < j.tiles && i < ahead; t += j.clusters)
+        for (int ks = s0; ks < s1 && i < ahead; ks++) weights(i++, t, ks);
       wait_for_previous();
       int st = 0;
       uint32_t ph = 0, used = 0, last_par = 0;
@@ -130,8 +136,9 @@ __global__ void __launch_bounds__(Few<NG>::threads, 1)
       i = 0;
       for (int t = first; ok && t < j.tiles; t += j.clusters)
         for (int ks = s0; ks < s1; ks++, i++) {
-          if (i >= F::stages) {
-            if (!mbar_wait_bounded(&empty[st], ph ^ 1, s_abort, kWaitLimit)) {
+          if (i >= ahead) {
+            if (i >= F::stages &&
+                !mbar_wait_bounded(&empty[st], ph ^ 1, s_abort, kWaitLimit)) {
               ok = gave_up();
               break;
             }

@@ -54,45 +54,65 @@ __device__ __forceinline__ void load8(const void *p, size_t i, int n, bool vec, 
   }
 }
 
-// rint(x / s), clamped: the quotient is the correctly rounded one, so that a
-// plain division gives the same integers.
-__device__ __forceinline__ int quant(float x, float s) {
-  return (int)fminf(fmaxf(rintf(__fdiv_rn(x, s)), -127.f), 127.f);
+// Eight times rint(x / s), clamped, as FP32: the quotient is the correctly rounded
+// one, so that a plain division gives the same integers.  A division takes some 15
+// instructions and would bound the kernel, so x times r = 1 / s decides first: it is
+// off by less than 1.6e-5, the rounded quotient itself by less than 8e-6, and only where
+// one of the eight lies nearer than 1e-4 to a tie are they divided.  r is 0 where 1 / s
+// could leave the normal numbers: all are divided then.
+constexpr float kRound = 12582912.0f;  // 1.5 2^23
+__device__ __forceinline__ void quant8(const float (&x)[8], float s, float r, float (&c)[8]) {
+  float off = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const float y = x[i] * r;
+    c[i] = (y + kRound) - kRound;
+    off = fmaxf(off, fabsf(y - c[i]));
+  }
+  if (off > 0.4999f || r == 0.f)
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      c[i] = fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -127.f), 127.f);
 }
 
 constexpr int kQThreads = 256;
 
-// 8 consecutive integers of which n are stored (vec: aligned for one store)
-__device__ __forceinline__ void store8(int8_t *dst, const int (&c)[8], int n, bool vec) {
-  if (vec && n >= 8) {
-    uint32_t w[2] = {0, 0};
+// 8 consecutive integers (as FP32) of which n are stored (vec: aligned for one store)
+__device__ __forceinline__ void store8(int8_t *dst, const float (&c)[8], int n, bool vec) {
+  uint32_t b[8];  // the integer is the low byte
 #pragma unroll
-    for (int i = 0; i < 8; i++) w[i >> 2] |= ((uint32_t)c[i] & 0xFFu) << (8 * (i & 3));
+  for (int i = 0; i < 8; i++) b[i] = __float_as_uint(c[i] + kRound);
+  if (vec && n >= 8) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+      w[i] = __byte_perm(__byte_perm(b[4 * i], b[4 * i + 1], 0x0040),
+                         __byte_perm(b[4 * i + 2], b[4 * i + 3], 0x0040), 0x5410);
     *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; i++)
-      if (i < n) dst[i] = (int8_t)c[i];
+      if (i < n) dst[i] = (int8_t)b[i];
   }
 }
-__device__ __forceinline__ void store8(__half *dst, const int (&c)[8], int n, bool vec) {
+__device__ __forceinline__ void store8(__half *dst, const float (&c)[8], int n, bool vec) {
   if (vec && n >= 8) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      const __half2 h = __floats2half2_rn((float)c[2 * i], (float)c[2 * i + 1]);
+      const __half2 h = __floats2half2_rn(c[2 * i], c[2 * i + 1]);
       w[i] = reinterpret_cast<const uint32_t &>(h);
     }
     *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; i++)
-      if (i < n) dst[i] = __float2half_rn((float)c[i]);
+      if (i < n) dst[i] = __float2half_rn(c[i]);
   }
 }
 
-// One CTA a row: the row's largest magnitude, then its integers (the second
-// read comes from cache).  The maximum is taken of the bits of |x|, which order
+// One CTA a row: the row's largest magnitude, then its integers; 4096 entries stay in
+// registers between, the second read of the others comes from cache.  The maximum is taken of the bits of |x|, which order
 // as the values do and put Inf and NaN above every number.  Q: int8_t, or __half
 // for the products' tokens.  Also zeroes the nzero counters of the kernel that
 // follows, which may start before this one ends and waits for its end.
@@ -106,12 +126,25 @@ __global__ void __launch_bounds__(kQThreads)
   if (row == 0)
     for (int i = tid; i < nzero; i += kQThreads) zero[i] = 0;
   const char *x = static_cast<const char *>(X) + (size_t)row * ldx * (DT == OS2_F32 ? 4 : 2);
+  constexpr int STEP = kQThreads * 8, KEPT = 2;
   uint32_t top = 0;
-  for (int h = tid * 8; h < k; h += kQThreads * 8) {
-    float v[8];
-    load8<DT>(x, h, k - h, vecx, v);
+  auto larger = [&](const float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; i++) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  };
+  float kept[KEPT][8];
+#pragma unroll
+  for (int i = 0; i < KEPT; i++) {
+    const int h = i * STEP + tid * 8;
+    if (h < k) {
+      load8<DT>(x, h, k - h, vecx, kept[i]);
+      larger(kept[i]);
+    }
+  }
+  for (int h = KEPT * STEP + tid * 8; h < k; h += STEP) {
+    float v[8];
+    load8<DT>(x, h, k - h, vecx, v);
+    larger(v);
   }
   top = __reduce_max_sync(0xffffffffu, top);
   if ((tid & 31) == 0) s_top[tid >> 5] = top;
@@ -121,14 +154,27 @@ __global__ void __launch_bounds__(kQThreads)
   const bool finite = top < 0x7F800000u;
   const float s = __fdiv_rn(__uint_as_float(top), 127.f);
   if (tid == 0) scale[row] = finite ? s : __uint_as_float(0x7FC00000u);
+  const float r = s > 1e-30f && finite ? __frcp_rn(s) : 0.f;
   Q *dst = q + (size_t)row * ldq;
-  for (int h = tid * 8; h < k; h += kQThreads * 8) {
+  auto put = [&](int h, const float (&v)[8]) {
+    float c[8];
+    if (finite && s > 0.f) {
+      quant8(v, s, r, c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i++) c[i] = 0.f;
+    }
+    store8(dst + h, c, k - h, vecq);
+  };
+#pragma unroll
+  for (int i = 0; i < KEPT; i++) {
+    const int h = i * STEP + tid * 8;
+    if (h < k) put(h, kept[i]);
+  }
+  for (int h = KEPT * STEP + tid * 8; h < k; h += STEP) {
     float v[8];
     load8<DT>(x, h, k - h, vecx, v);
-    int c[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) c[i] = finite && s > 0.f ? quant(v[i], s) : 0;
-    store8(dst + h, c, k - h, vecq);
+    put(h, v);
   }
 }
 
@@ -142,16 +188,19 @@ __global__ void __launch_bounds__(kQThreads)
     for (int i = tid; i < nzero; i += kQThreads) zero[i] = 0;
   const int8_t *a = A + (size_t)row * lda;
   for (int h = tid * 8; h < k; h += kQThreads * 8) {
-    int c[8];
+    __half *to = dst + (size_t)row * pitch + h;
     if (vec && h + 8 <= k) {
       const uint2 w = *reinterpret_cast<const uint2 *>(a + h);
-#pragma unroll
-      for (int i = 0; i < 8; i++) c[i] = (int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+      uint4 o;
+      os2i8::widen(w.x, o.x, o.y);
+      os2i8::widen(w.y, o.z, o.w);
+      *reinterpret_cast<uint4 *>(to) = o;
     } else {
+      float c[8];
 #pragma unroll
-      for (int i = 0; i < 8; i++) c[i] = h + i < k ? a[h + i] : 0;
+      for (int i = 0; i < 8; i++) c[i] = h + i < k ? (float)a[h + i] : 0.f;
+      store8(to, c, k - h, true);
     }
-    store8(dst + (size_t)row * pitch + h, c, k - h, true);
   }
 }
 

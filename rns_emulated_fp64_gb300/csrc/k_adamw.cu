@@ -19,6 +19,9 @@
 // CTAs an SM rather than five are worth 6 %, conversions are additions of 2^23 and
 // 1.5 2^23 instead of I2F and F2I, which run at a quarter of the rate, and the
 // exact rounding is taken only where the fast one is in doubt.
+// Measured: FP32 moments, FP32 parameters, BF16 gradients, 268 M elements 979 us (7.1
+// TB/s); 8-bit moments, BF16 both, 150 M elements 387 us (3.9 TB/s: instruction issue,
+// 77 % busy); 24 tensors of 0.3 M in all 3.8 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, Q8 ? 6 : 1) k_adamw(const __grid_con
 }
 
 // Four consecutive elements a lane and run, so that a store instruction covers
-// whole lines; four runs in flight.
+// whole lines; four runs in flight.  150 M elements 224 us (6.7 TB/s).
 constexpr int kMomentRuns = 4;
 __global__ void __launch_bounds__(kThreads)
     k_moments(long long numel, const int8_t *cm, const float *am, const uint8_t *cv,

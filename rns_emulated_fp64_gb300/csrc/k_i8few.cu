@@ -3,11 +3,12 @@
 // A CTA streams its share of the weights through a ring of TMA copies (up to 200
 // KB an SM in flight, whatever the registers hold) with the tokens' matching
 // terms beside them.  Eight warps take 16 channels each of a stage of 128 channels
-// x 128 terms (up to 16 tokens, two groups of eight the stages in turn: the group that
-// works reads shared memory while the other multiplies): a lane reads 16 bytes of two channels at a time, widens
-// them to FP16 in registers (exact) and multiplies with mma.sync.m16n8k16, whose
-// fragments are the lanes' own bytes: the 16 terms of an instruction may be any,
-// as long as the tokens' are the same, so lane t's 16 consecutive bytes serve four
+// x 128 terms (up to 16 tokens, two groups of eight take the stages in turn: one reads
+// shared memory while the other multiplies).  A lane reads 16 bytes of two channels
+// at a time, widens them to FP16 in registers (exact) and multiplies with
+// mma.sync.m16n8k16, whose fragments are the lanes' own bytes: the 16 terms of an
+// instruction may be any, as long as the tokens' are the same, so lane t's 16
+// consecutive bytes serve four
 // instructions.  tcgen05 would need the FP16 weights back in shared memory
 // (k_i8tc.cu: half the rate for 16 tokens).  FP32 accumulators are exact for 1024
 // terms (2^24); they are emptied into int32 after those.

@@ -29,6 +29,8 @@
 // it needs.  Every wait is bounded, as in mm2.cuh.  Between the CTAs of
 // a pair go arrivals without a release at cluster scope (ptx.cuh); with it, every
 // stage waited for its fence: 1985 us instead of 1075 for 8192 x 4096 x 16384.
+// Measured with quantising: 684 us for that (1.6 PFLOP/s, 0.84 of cuBLAS's BF16 burst), 21 us
+// for 65 tokens and 4096 x 4096 weights, 22.9 for 205, 5003 x 1777 and rows that are copied first.
 #include "i8.cuh"
 
 using namespace os2i8;

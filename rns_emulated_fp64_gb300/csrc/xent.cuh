@@ -37,8 +37,8 @@ struct XentFewArgs {
   float2 *part;                // [n][parts]
   int *status;
 };
-// Up to this many rows of H, the forward pass is k_xent_few: 29 us against 37 with
-// the tiles of k_xent.cu for 8 rows (k = 2048, v = 32000), 32 for 16; as much for 32.
+// Up to this many rows of H, the forward pass is k_xent_few: 28 us for one or 8 rows and 31
+// for 16 (k = 2048, v = 32000), against 37 to 39 with the tiles of k_xent.cu for 17 to 64.
 constexpr int kXentFew = 16;
 // At most one pair a row and SM; *parts receives the pairs of a row.
 cudaError_t launch_xent_few(const XentFewArgs &a, int *parts, cudaStream_t s);

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kQThreads)
             bool vecq, unsigned *zero, int nzero) {
   __shared__ uint32_t s_top[kQThreads / 32];
   const int row = blockIdx.x, tid = threadIdx.x;
-  next_may_start();
+  start_call();
   if (row == 0)
     for (int i = tid; i < nzero; i += kQThreads) zero[i] = 0;
   const char *x = static_cast<const char *>(X) + (size_t)row * ldx * (DT == OS2_F32 ? 4 : 2);
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kQThreads)
 __global__ void __launch_bounds__(kQThreads)
     k_widen_tokens(int k, const int8_t *A, long lda, __half *dst, long pitch, bool vec,
                    unsigned *zero, int nzero) {
-  next_may_start();
+  start_call();
   const int row = blockIdx.x, tid = threadIdx.x;
   if (row == 0)
     for (int i = tid; i < nzero; i += kQThreads) zero[i] = 0;
@@ -253,12 +253,12 @@ cudaError_t quantize(int m, int k, int dtype, const void *X, long ldx, Q *q, lon
                      float *scale, cudaStream_t s, unsigned *zero = nullptr, int nzero = 0) {
   const bool vecx = aligned(X, 16) && (ldx * elem_size(dtype)) % 16 == 0;
   const bool vecq = aligned(q, 8 * sizeof(Q)) && ldq % 8 == 0;
-#define QUANT(DT) k_quant<DT, Q><<<m, kQThreads, 0, s>>>(k, X, ldx, q, ldq, scale, vecx, vecq, zero, nzero)
-  if (dtype == OS2_F32) QUANT(OS2_F32);
-  else if (dtype == OS2_BF16) QUANT(OS2_BF16);
-  else QUANT(OS2_F16);
-#undef QUANT
-  return cudaGetLastError();
+  auto launch = [&](auto kernel) {
+    return launch_after(kernel, m, kQThreads, 0, s, k, X, ldx, q, ldq, scale, vecx, vecq, zero, nzero);
+  };
+  if (dtype == OS2_F32) return launch(k_quant<OS2_F32, Q>);
+  if (dtype == OS2_BF16) return launch(k_quant<OS2_BF16, Q>);
+  return launch(k_quant<OS2_F16, Q>);
 }
 
 // |sum| <= k 2^14 stays below 2^31
@@ -394,10 +394,12 @@ extern "C" os2_status os2_i8gemm(int m, int n, int k, const int8_t *A, int lda,
     return cudaGetLastError() == cudaSuccess ? OS2_OK : OS2_ERR_CUDA;
   }
   char *ws = static_cast<char *>(workspace);
-  k_widen_tokens<<<m, kQThreads, 0, s>>>(k, A, lda, reinterpret_cast<__half *>(ws + L.tokens),
-                                         L.pitch, aligned(A, 8) && lda % 8 == 0,
-                                         reinterpret_cast<unsigned *>(ws + L.done), L.counters);
-  const cudaError_t e = product(m, n, k, L, ws, a_scale, B, ldb, b_scale, bias, C, ldc, out_dtype,
+  cudaError_t e = launch_after(k_widen_tokens, m, kQThreads, 0, s, k, A, lda,
+                               reinterpret_cast<__half *>(ws + L.tokens), L.pitch,
+                               aligned(A, 8) && lda % 8 == 0,
+                               reinterpret_cast<unsigned *>(ws + L.done), L.counters);
+  if (e != cudaSuccess) return OS2_ERR_CUDA;
+  e = product(m, n, k, L, ws, a_scale, B, ldb, b_scale, bias, C, ldc, out_dtype,
                                 status, s);
   return e == cudaSuccess ? OS2_OK : OS2_ERR_CUDA;
 }

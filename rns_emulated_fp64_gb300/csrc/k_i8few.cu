@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(Few<NG>::threads, 1)
     tma_prefetch_desc(&mapW);
     tma_prefetch_desc(&mapT);
   }
+  next_may_start();
   __syncthreads();
   cluster_arrive();  // waited for before anything is sent to another CTA
 

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kPrepThreads) k_xent_prep(const Prep p) {
   __shared__ int s_pos[kPrepThreads], s_warp[kPrepThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r0 = blockIdx.x * p.rows_cta, r1 = min(p.n, r0 + p.rows_cta);
-  next_may_start();
+  start_call();
   if (tid < 2) s_sum[tid] = 0;
   __syncthreads();
   int before = 0, total = 0;
@@ -661,17 +661,16 @@ cudaError_t prepare(const Layout &L, Prep &p, const uint16_t *&W, long &ldw, voi
   // few rows: one a CTA; at least 16 CTAs where the rows past the count are zeroed
   p.rows_cta = (p.n + 4 * os2_sm_count() - 1) / (4 * os2_sm_count());
   const int grid = std::max((p.n + p.rows_cta - 1) / p.rows_cta, p.grad ? 16 : 1);
-  k_xent_prep<<<grid, kPrepThreads, 0, s>>>(p);
-  if (!tma_rows(W, ldw)) {
+  cudaError_t e = launch_after(k_xent_prep, grid, kPrepThreads, 0, s, p);
+  if (e == cudaSuccess && !tma_rows(W, ldw)) {
     uint16_t *wc = at<uint16_t>(ws, L.Wc);
-    const cudaError_t e = launch_after(
+    e = launch_after(
         k_repack, (int)std::min<long>((L.kp / 8 * p.v + 255) / 256, 16L * os2_sm_count()), 256, 0, s,
         W, ldw, wc, L.kp, p.v, p.k);
-    if (e != cudaSuccess) return e;
     W = wc;
     ldw = L.kp;
   }
-  return cudaGetLastError();
+  return e;
 }
 
 template <bool BF16>

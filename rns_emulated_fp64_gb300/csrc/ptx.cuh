@@ -83,6 +83,14 @@ __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// A call's first kernel: launched while the kernel in front of it ends, it waits
+// for that before it does anything, and before it lets the next one begin, which may
+// then count on all that lies before the call.
+__device__ __forceinline__ void start_call() {
+  wait_for_previous();
+  next_may_start();
+}
+
 // Moves registers between the warpgroups of a block (all warps of a warpgroup
 // execute it; the sum over the warpgroups must not pass what the block was
 // launched with).

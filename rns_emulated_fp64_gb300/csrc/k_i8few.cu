@@ -25,9 +25,9 @@
 // tokens: they are inputs of the call, and nothing in front of that kernel can be
 // writing them still.  Every wait is bounded, as in mm2.cuh.
 //
-// Measured with the quantising launch: one token 8.3 us for 4096 x 4096 weights, 17.3
-// for 14336 x 4096 and 17.9 for 32000 x 2048 (3.7 TB/s; a kernel that only reads takes 6.2, 12.4
-// and 13.6); 12 tokens 9.3, 18.5 and 19.6.  The rest is the start of the ring, 500 cycles
+// Measured with the quantising launch: one token 7.6 us for 4096 x 4096 weights, 16.4
+// for 14336 x 4096 and 16.8 for 32000 x 2048 (3.9 TB/s; a kernel that only reads takes 6.2,
+// 12.4 and 13.6); 12 tokens 8.8, 17.9 and 18.7; 64 tokens 16.4, 33.4 and 35.7.  The rest is the start of the ring, 500 cycles
 // of shared memory a stage (weights in and out, tokens) against 740 of DRAM, and tiles
 // that do not divide by the SMs.
 #include "i8.cuh"
@@ -42,7 +42,8 @@ constexpr uint32_t kFewW = 128 * kStageK;        // a stage's weights
 template <int NG>
 struct Few {
   // Up to 16 tokens, two groups of warps take the stages in turn: 17.9 us against 19.1
-  // for one token and 32000 x 2048 weights, 8.3 against 8.8 for 4096 x 4096; above,
+  // for one token and 32000 x 2048 weights (before the ring was filled step by step), 8.3
+  // against 8.8 for 4096 x 4096; above,
   // their exchange costs more than it gives (25.1 against 24.2 for 32 tokens).
   static constexpr int groups = NG <= 2 ? 2 : 1;
   static constexpr int all = kFewWarps * groups, threads = 32 * all + 32;
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(Few<NG>::threads, 1)
       // stream does not ask for the whole ring at first: memory serves all that is asked for
       // side by side, so the first stage would be there as late as the last, and the
       // tokens behind it (32000 x 2048, one token: 18.0 us with the whole ring, 16.7 with
-      // 6 stages; a CTA that has its whole share in the ring: 8.5 with all 8 of them, 8.8 with 6).
+      // 6 stages; 4096 x 4096, whose 8 stages a CTA fit in the ring: 8.5 with all, 8.8 with 6).
       const int share = (j.tiles - first + j.clusters - 1) / j.clusters * (s1 - s0);
       const int ahead = share <= F::stages ? F::stages : min(6, F::stages);
       int i = 0;

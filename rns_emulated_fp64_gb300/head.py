@@ -70,7 +70,8 @@ def xent(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, ignore_index: i
 
     H: n x k, W: v x k, bfloat16 or float16; labels: n int64.  Returns (loss,
     lse), float32, one value a row; 0 for rows labelled ignore_index.  A label
-    out of range is reported by ``get_status`` (ERR_RANGE)."""
+    out of range is reported by ``get_status`` (ERR_RANGE).  A width that is a
+    multiple of 8 (rows of W on 16-byte boundaries) saves a copy of W in each call."""
     return _run(load_head().xent, stream, H, H, W, labels, ignore_index, workspace)
 
 

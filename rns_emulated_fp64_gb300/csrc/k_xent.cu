@@ -323,32 +323,40 @@ struct StatsEpi {
   __device__ __forceinline__ void finish() {}
 };
 
-// A warp's block of 32 rows of 64 bytes (16 x 4 bytes a lane, its row) leaves by TMA
-// to (col, row0, layer), stored or added; two blocks of the scratch memory take turns.
-__device__ __forceinline__ void send_block(const CUtensorMap *map, uint8_t *scratch, int turn,
-                                           const uint4 (&v)[4], int col, int row0, int layer,
-                                           bool add) {
-  const int lane = threadIdx.x & 31;
-  uint8_t *block = scratch + (turn & 1) * 2048;
-  if (lane == 0) bulk_wait_read<1>();  // the block before the last has left
-  __syncwarp();
+// A warp's blocks of 32 rows of 64 bytes (16 x 4 bytes a lane, its row) leave by TMA to
+// (col, row0, layer), stored or added.  Two blocks of the scratch memory take turns over
+// all that the warp sends, from tile to tile too: a tile may end after an odd number, and a
+// turn that began anew there would write the block whose copy is the one still allowed to be
+// reading.
+struct BlockSender {
+  int turn = 0;
+
+  __device__ __forceinline__ void send(const CUtensorMap *map, uint8_t *scratch,
+                                       const uint4 (&v)[4], int col, int row0, int layer,
+                                       bool add) {
+    const int lane = threadIdx.x & 31;
+    uint8_t *block = scratch + turn * 2048;
+    turn ^= 1;
+    if (lane == 0) bulk_wait_read<1>();  // the block before the last has left
+    __syncwarp();
 #pragma unroll
-  for (int q = 0; q < 4; q++)
-    *reinterpret_cast<uint4 *>(block + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) = v[q];
-  fence_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    if (add)
-      tma_add_3d(map, block, col, row0, layer);
-    else
-      tma_store_3d(map, block, col, row0, layer);
-    bulk_commit();
+    for (int q = 0; q < 4; q++)
+      *reinterpret_cast<uint4 *>(block + lane * 64 + ((q ^ (lane >> 1 & 3)) << 4)) = v[q];
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (add)
+        tma_add_3d(map, block, col, row0, layer);
+      else
+        tma_store_3d(map, block, col, row0, layer);
+      bulk_commit();
+    }
   }
-}
-__device__ __forceinline__ void blocks_sent() {
-  if ((threadIdx.x & 31) == 0) bulk_wait_all();
-  __syncwarp();
-}
+  __device__ __forceinline__ void finish() {
+    if ((threadIdx.x & 31) == 0) bulk_wait_all();
+    __syncwarp();
+  }
+};
 
 // Backward: D of one piece (columns v0 .. v0 + v) in the operands' type.  Its
 // rounding is that of one operand of a product whose sums are FP32, as H's and
@@ -360,6 +368,7 @@ struct GradEpi {
   const int *label;
   const float *lse, *grad, *scale;
   int v0, v;
+  BlockSender sender = {};
 
   __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, bool, bool, int m,
                                        const CUtensorMap *mapD, uint8_t *scratch, int *) {
@@ -397,10 +406,10 @@ struct GradEpi {
                           pack2<BF16>(x[8 * q + 2], x[8 * q + 3]),
                           pack2<BF16>(x[8 * q + 4], x[8 * q + 5]),
                           pack2<BF16>(x[8 * q + 6], x[8 * q + 7]));
-      send_block(mapD, scratch, g, o, col0 + g * 32, row0, 0, false);
+      sender.send(mapD, scratch, o, col0 + g * 32, row0, 0, false);
     }
   }
-  __device__ __forceinline__ void finish() { blocks_sent(); }
+  __device__ __forceinline__ void finish() { sender.finish(); }
 };
 
 // dW, and dH where it comes out of one product: scaled back, rounded once, to the
@@ -419,6 +428,7 @@ struct StoreEpi {
   const float *scale;
   int rows, n;          // of `out`
   bool vec;             // rows of `out` are 16-byte aligned
+  BlockSender sender = {};
 
   __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, bool, bool, int m,
                                        const CUtensorMap *mapD, uint8_t *scratch, int *status) {
@@ -446,7 +456,7 @@ struct StoreEpi {
       }
       if constexpr (TMA) {
         // (rows from m on are cut off by the map)
-        send_block(mapD, scratch, g, v, col0 + g * 32, row0, 0, false);
+        sender.send(mapD, scratch, v, col0 + g * 32, row0, 0, false);
       } else {
 #pragma unroll
         for (int q = 0; q < 4; q++) *reinterpret_cast<uint4 *>(scratch + lane * 80 + q * 16) = v[q];
@@ -473,7 +483,7 @@ struct StoreEpi {
     }
   }
   __device__ __forceinline__ void finish() {
-    if (TMA) blocks_sent();
+    if (TMA) sender.finish();
   }
 };
 
@@ -484,6 +494,7 @@ struct StoreEpi {
 // their own rows, now 11.5.
 struct SumEpi {
   bool add;
+  BlockSender sender = {};
 
   __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int split, bool, bool,
                                        int m, const CUtensorMap *mapD, uint8_t *scratch, int *) {
@@ -498,10 +509,10 @@ struct SumEpi {
       const uint4 v[4] = {make_uint4(r[0], r[1], r[2], r[3]), make_uint4(r[4], r[5], r[6], r[7]),
                           make_uint4(r[8], r[9], r[10], r[11]),
                           make_uint4(r[12], r[13], r[14], r[15])};
-      send_block(mapD, scratch, g, v, col0 + g * 16, row0, split, add);
+      sender.send(mapD, scratch, v, col0 + g * 16, row0, split, add);
     }
   }
-  __device__ __forceinline__ void finish() { blocks_sent(); }
+  __device__ __forceinline__ void finish() { sender.finish(); }
 };
 
 // dH from those sums, the parts in their order: four columns a thread, eight parts

@@ -188,12 +188,24 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+def _ld(X, name) -> int:
+    """The leading dimension of a 2-D tensor whose rows do not overlap (an
+    expanded tensor's rows do); the stride of a single row means nothing."""
+    rows, cols = X.shape
+    if rows <= 1:
+        return max(cols, 1)
+    if X.stride(0) < cols:
+        raise ValueError(f"{name} must have rows that do not overlap: row stride {X.stride(0)} of "
+                         f"{cols} entries")
+    return max(X.stride(0), 1)
+
+
 def _kmat(X, name):
     """float64 CUDA matrix whose rows are contiguous; returns (X, ld)."""
     if not (X.is_cuda and X.dtype == torch.float64 and X.dim() == 2 and
             (X.stride(1) == 1 or X.shape[1] <= 1)):
         raise ValueError(f"{name} must be a 2-D float64 CUDA tensor with contiguous rows")
-    return X, max(X.stride(0), max(X.shape[1], 1))
+    return X, _ld(X, name)
 
 
 def moduli(num_moduli: int) -> list[int]:
@@ -279,7 +291,7 @@ def gemm(A: torch.Tensor, Bt: torch.Tensor, num_moduli: int = 14, mode="fast", o
         raise ValueError("inner dimensions differ")
     if out is None:
         out = torch.empty((m, n), dtype=torch.float64, device=A.device)
-    ldc = max(out.stride(0), max(n, 1))
+    ldc = _ld(out, "out")
     need = workspace_size(m, n, k, num_moduli, mode)
     if workspace is None:
         workspace = alloc_workspace(need, A.device)
@@ -304,10 +316,9 @@ def sgemm(A: torch.Tensor, Bt: torch.Tensor, num_moduli: int = 7, mode="fast", o
     need = workspace_size(m, n, k, num_moduli, mode)
     if workspace is None:
         workspace = alloc_workspace(need, A.device)
-    st = load().os2_sgemm(m, n, k, _ptr(A), max(A.stride(0), max(k, 1)), _ptr(Bt),
-                          max(Bt.stride(0), max(k, 1)), _ptr(out), max(out.stride(0), max(n, 1)),
-                          num_moduli, _mode(mode), _ptr(workspace), workspace.numel(),
-                          _stream(stream))
+    st = load().os2_sgemm(m, n, k, _ptr(A), _ld(A, "A"), _ptr(Bt), _ld(Bt, "Bt"), _ptr(out),
+                          _ld(out, "out"), num_moduli, _mode(mode), _ptr(workspace),
+                          workspace.numel(), _stream(stream))
     _check(st, "os2_sgemm")
     return out
 
@@ -338,9 +349,8 @@ def zgemm(A: torch.Tensor, Bt: torch.Tensor, num_moduli: int = 16, mode="fast", 
         workspace = alloc_workspace(complex_workspace_size(m, n, k, num_moduli, mode, single),
                                     A.device)
     fn = load().os2_cgemm if single else load().os2_zgemm
-    st = fn(m, n, k, _ptr(A), max(A.stride(0), max(k, 1)), _ptr(Bt), max(Bt.stride(0), max(k, 1)),
-            _ptr(out), max(out.stride(0), max(n, 1)), num_moduli, _mode(mode), _ptr(workspace),
-            workspace.numel(), _stream(stream))
+    st = fn(m, n, k, _ptr(A), _ld(A, "A"), _ptr(Bt), _ld(Bt, "Bt"), _ptr(out), _ld(out, "out"),
+            num_moduli, _mode(mode), _ptr(workspace), workspace.numel(), _stream(stream))
     _check(st, "os2_cgemm" if single else "os2_zgemm")
     return out
 
@@ -359,13 +369,12 @@ def gemm_host(A, Bt, C, num_moduli=14, mode="fast", workspace=None, stream=None)
             raise ValueError(f"{nm} must be a 2-D float64 host tensor with contiguous rows")
     m, k = A.shape
     n = Bt.shape[0]
+    lda, ldb, ldc = _ld(A, "A"), _ld(Bt, "Bt"), _ld(C, "C")
     need = host_workspace_size(m, n, k, num_moduli, mode)
     if workspace is None:
         workspace = alloc_workspace(need)
-    st = load().os2_gemm_host(m, n, k, _ptr(A), max(A.stride(0), max(k, 1)), _ptr(Bt),
-                              max(Bt.stride(0), max(k, 1)), _ptr(C), max(C.stride(0), max(n, 1)),
-                              num_moduli, _mode(mode), _ptr(workspace), workspace.numel(),
-                              _stream(stream))
+    st = load().os2_gemm_host(m, n, k, _ptr(A), lda, _ptr(Bt), ldb, _ptr(C), ldc, num_moduli,
+                              _mode(mode), _ptr(workspace), workspace.numel(), _stream(stream))
     _check(st, "os2_gemm_host")
     return C
 
@@ -496,7 +505,7 @@ def gemm_exponents(A: torch.Tensor, Bt: torch.Tensor, num_moduli: int, e: torch.
         workspace = alloc_workspace(workspace_size(m, n, k, num_moduli, "fast"), A.device)
     e = e.to(torch.int32).contiguous()
     f = f.to(torch.int32).contiguous()
-    _check(load().os2_gemm_exponents(m, n, k, _ptr(A), lda, _ptr(Bt), ldb, _ptr(C), C.stride(0),
+    _check(load().os2_gemm_exponents(m, n, k, _ptr(A), lda, _ptr(Bt), ldb, _ptr(C), _ld(C, "out"),
                                      int(num_moduli), _ptr(e), _ptr(f), _ptr(workspace),
                                      workspace.numel(), _stream(stream)), "os2_gemm_exponents")
     return C
@@ -519,7 +528,7 @@ def gemm_noalloc(A: torch.Tensor, Bt: torch.Tensor, num_moduli: int = 14, mode="
         raise ValueError("inner dimensions differ")
     if out is None:
         out = torch.empty((m, n), dtype=torch.float64, device=A.device)
-    ldc = max(out.stride(0), max(n, 1))
+    ldc = _ld(out, "out")
     st = load().os2_gemm_noalloc(m, n, k, _ptr(A), lda, _ptr(Bt), ldb, _ptr(out), ldc,
                                  num_moduli, _mode(mode), _stream(stream))
     _check(st, "os2_gemm_noalloc")

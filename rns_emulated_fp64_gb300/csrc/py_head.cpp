@@ -56,18 +56,20 @@ int as_int(int64_t x, const char *name) {
   return int(x);
 }
 
-// A 2-D CUDA tensor with contiguous rows.
+// A 2-D CUDA tensor with contiguous rows that do not overlap.
 struct Rows {
   int m, k, ld;
   void *p;
 };
 
 Rows rows(const Tensor &x, const char *name, bool type_ok, const char *types) {
-  TORCH_CHECK_VALUE(x.is_cuda() && x.dim() == 2 && type_ok, name, " must be a 2-D CUDA tensor of ", types);
+  TORCH_CHECK_VALUE(x.dim() == 2 && type_ok, name, " must be a 2-D CUDA tensor of ", types);
   const int64_t m = x.size(0), k = x.size(1), ld = x.stride(0);
   TORCH_CHECK_VALUE(k <= 1 || x.stride(1) == 1, name, " must have contiguous rows");
-  // the stride of a single row means nothing
-  return {as_int(m, name), as_int(k, name), as_int(m > 1 && ld > k ? ld : std::max<int64_t>(k, 1), name), x.data_ptr()};
+  // (an expanded tensor's rows do; the stride of a single row means nothing)
+  TORCH_CHECK_VALUE(m <= 1 || ld >= k, name, " must have rows that do not overlap: row stride ", ld, " of ", k, " entries");
+  TORCH_CHECK_VALUE(x.is_cuda(), name, " must be a 2-D CUDA tensor of ", types);
+  return {as_int(m, name), as_int(k, name), as_int(std::max<int64_t>(m > 1 ? ld : k, 1), name), x.data_ptr()};
 }
 
 Tensor vec(PyObject *o, const char *name, int64_t n, at::ScalarType t, c10::Device dev) {

@@ -31,7 +31,11 @@ def _run(f, stream, like, *args):
         index = like.get_device()
         if index < 0:
             raise ValueError("every tensor must be on one CUDA device")
-        stream = torch.cuda.ExternalStream(int(stream), device=index)
+        # The default stream has the handles 0 and 1 (the legacy one), neither of which
+        # ExternalStream takes for it.
+        handle = int(stream)
+        stream = (torch.cuda.default_stream(index) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device=index))
     with torch.cuda.stream(stream):
         return f(*args)
 

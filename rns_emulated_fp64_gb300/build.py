@@ -83,7 +83,8 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     _build_debug/)."""
     bdir, lib = (BUILD_DEBUG, LIB_DEBUG) if debug else (BUILD, LIB)
     os.makedirs(bdir, exist_ok=True)
-    headers = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    headers = [h for d, ext in ((CSRC, "*.cuh"), (CSRC, "*.h"), (os.path.join(ROOT, "include"), "*.h"))
+               for h in glob.glob(os.path.join(d, ext))]
     srcs = sources()
     if not force and not _stale(lib, srcs + headers + [__file__]):
         build_head()

@@ -31,28 +31,13 @@
 // of shared memory a stage (weights in and out, tokens) against 740 of DRAM, and tiles
 // that do not divide by the SMs.
 #include "i8.cuh"
+#include "i8_ring.h"
 
 using namespace os2i8;
 
 namespace {
 
-constexpr int kFewWarps = 8;                     // of a group, 16 channels each
-constexpr uint32_t kFewW = 128 * kStageK;        // a stage's weights
-
-template <int NG>
-struct Few {
-  // Up to 16 tokens, two groups of warps take the stages in turn: 17.9 us against 19.1
-  // for one token and 32000 x 2048 weights (before the ring was filled step by step), 8.3
-  // against 8.8 for 4096 x 4096; above,
-  // their exchange costs more than it gives (25.1 against 24.2 for 32 tokens).
-  static constexpr int groups = NG <= 2 ? 2 : 1;
-  static constexpr int all = kFewWarps * groups, threads = 32 * all + 32;
-  static constexpr uint32_t block = NG * 8 * kBK * 2;        // one k-block of the tokens
-  static constexpr uint32_t stage = kFewW + 2 * block;
-  static constexpr uint32_t part = all * NG * 32 * 16;  // a tile's sums, one side
-  static constexpr int stages = (int)((227 * 1024 - 1024 - 512 - 2 * part) / stage);
-  static constexpr size_t smem = 1024 + (size_t)stages * stage + 2 * part + 512;
-};
+static_assert(kFewW == 128 * kStageK && Few<1>::block == 8 * kBK * 2, "a stage of the ring");
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {

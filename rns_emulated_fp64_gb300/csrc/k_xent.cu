@@ -64,7 +64,7 @@ struct Prep {
   // backward
   const float *lse_in, *grad;
   float *lse_c, *grad_c; // [n]
-  float *scale;          // {1 / max |g|, 2^-E max |g|}
+  float *scale;          // {1 / max |g|, 2^-E max |g|}, g finite
   bool f16;
   uint16_t *dH;          // zeroed for the others (may be null)
   long lddh;
@@ -94,7 +94,10 @@ __global__ void __launch_bounds__(kPrepThreads) k_xent_prep(const Prep p) {
     const bool c = counts(p.labels[i], p);
     total += c;
     before += c && i < r0;
-    if (p.grad && c && blockIdx.x == 0) gmax = fmaxf(gmax, fabsf(p.grad[i]));
+    if (p.grad && c && blockIdx.x == 0) {
+      const float g = fabsf(p.grad[i]);
+      if (g < INFINITY) gmax = fmaxf(gmax, g);
+    }
   }
   before = __reduce_add_sync(0xffffffffu, before);
   total = __reduce_add_sync(0xffffffffu, total);
@@ -113,14 +116,15 @@ __global__ void __launch_bounds__(kPrepThreads) k_xent_prep(const Prep p) {
   if (blockIdx.x == 0 && tid == 0) {
     *p.count = nv;
     if (p.grad) {
-      // The logits' gradients are held divided by the largest |g| and times 2^E
+      // The logits' gradients are held divided by the largest finite |g| (a row whose g is
+      // not finite has no finite gradient, and takes nothing from the others) and times 2^E
       // (kGradExp).  Where all g are equal, as a mean's are, the entry of the label,
       // the largest of its row, then lies just below a power of two, where rounding
       // is finest: dH and dW are 1.2 times as far off as by their own rounding
       // alone, against 1.7 times for a g whose leading digits are just above one.
       float g = 0.f;
       for (int w = 0; w < kPrepThreads / 32; w++) g = fmaxf(g, s_max[w]);
-      if (!(g > 1e-30f && g < INFINITY)) g = 1.f;
+      if (!(g > 1e-30f)) g = 1.f;
       p.scale[0] = 1.f / g;
       p.scale[1] = g * exp2f((float)-(p.f16 ? kGradExp16 : kGradExpB));
     }

@@ -431,7 +431,7 @@ os2_status os2_i8linear(int m, int n, int k, int dtype, const void *X, int ldx, 
 
 /* Device workspace of os2_xent (backward = 0) and os2_xent_backward (1): the
  * packed rows of H and, in the backward pass, one piece of the logits'
- * gradients (at most 256 MB, or 2048 columns).  0 on bad args; W and ldw as in
+ * gradients, twice (at most 256 MB each, or 2048 columns).  0 on bad args; W and ldw as in
  * the call (their alignment decides; W is not read).  256-byte aligned. */
 size_t os2_xent_workspace_size(int n, int k, int v, const void *W, int ldw, int backward);
 
@@ -450,9 +450,10 @@ os2_status os2_xent(int n, int k, int v, int dtype, const void *H, int ldh, cons
 /* Its gradient: with d_iv = grad[i] (exp(z_iv - lse[i]) - [v = labels[i]]),
  * dH = D W and dW = D^T H, where grad[i] is the gradient of loss[i] and lse what
  * os2_xent returned.  The logits are computed again, a piece of the vocabulary
- * at a time; D is rounded to `dtype` (FP16 with a power-of-two scale), sums are
- * FP32, dH (n x k, lddh >= k) and dW (v x k, lddw >= k) of `dtype`, each rounded
- * once and overwritten.  dH or dW may be NULL.  Ignored rows have dH = 0 and no
+ * at a time; D is rounded to `dtype`, held times 2^14 (FP16) or 2^40 (BF16) and
+ * divided by max |grad|; in FP16 what is below 2^-38 of max |grad| vanishes from dW, what
+ * is below 2^-32 of a row's own |grad[i]| from its row of dH.  Sums are FP32, dH (n x k,
+ * lddh >= k) and dW (v x k, lddw >= k) of `dtype`, each rounded once and overwritten.  dH or dW may be NULL.  Ignored rows have dH = 0 and no
  * part in dW, whatever H and grad hold there. */
 os2_status os2_xent_backward(int n, int k, int v, int dtype, const void *H, int ldh, const void *W,
                              int ldw, const long long *labels, long long ignore_index,

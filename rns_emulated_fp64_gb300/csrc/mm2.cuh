@@ -68,6 +68,7 @@ struct Job {
   // and that starts after all this one reads is there: it begins on the SMs that
   // the other leaves free, and ends after it.
   bool beside = false;
+  const int *a_layer = nullptr;  // if set, the layer of A's map to take, known on the device only
 };
 
 __device__ __forceinline__ void set_status(int *status, int code) {
@@ -170,6 +171,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int stage = 0;
         uint32_t phase = 0, used = 0, last_par = 0;
         bool ok = true;
+        const int la = job.a_layer ? *job.a_layer : 0;
         for (int t = pair; ok && t < njobs; t += npairs) {
           int tm, tn;
           tile_coords(t % tiles, tiles_m, tiles_n, tm, tn);
@@ -189,10 +191,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               uint8_t *da = sA + stage * kOpBytes + h * kBlockBytes;
               uint8_t *db = sB + stage * kOpBytes + h * kBlockBytes;
               if (A_MN) {  // two boxes of 64 rows of the tile x 64 terms
-                tma_load_3d_pair(da, &mapA, fbar, ra, kx, 0);
-                tma_load_3d_pair(da + kBlockBytes / 2, &mapA, fbar, ra + 64, kx, 0);
+                tma_load_3d_pair(da, &mapA, fbar, ra, kx, la);
+                tma_load_3d_pair(da + kBlockBytes / 2, &mapA, fbar, ra + 64, kx, la);
               } else {
-                tma_load_3d_pair(da, &mapA, fbar, kx, ra, 0);
+                tma_load_3d_pair(da, &mapA, fbar, kx, ra, la);
               }
               if (B_MN) {
                 tma_load_3d_pair(db, &mapB, fbar, rb, kx, 0);
@@ -342,14 +344,14 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// A row-major matrix of 16-bit entries: `rows` rows of `cols` entries, `pitch`
-// entries apart.  mn: the terms run along the rows (box 64 x 64), else along
+// Row-major matrices (`layers` in turn) of 16-bit entries: `rows` rows of `cols` entries,
+// `pitch` entries apart.  mn: the terms run along the rows (box 64 x 64), else along
 // the columns (box 64 x box_rows).  base and pitch * 2 must be multiples of 16.
 inline bool make_map(CUtensorMap *map, const void *base, bool bf16, long cols, long rows,
-                     long pitch, bool mn, int box_rows = kHalf) {
+                     long pitch, bool mn, int box_rows = kHalf, int layers = 1) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)layers};
   cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)pitch * 2 * (cuuint64_t)rows};
   cuuint32_t box[3] = {(cuuint32_t)kBK, (cuuint32_t)(mn ? kBK : box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};

@@ -131,6 +131,15 @@ Tensor workspace(PyObject *o, size_t need, c10::Device dev, cudaStream_t stream)
   return ws;
 }
 
+// A tensor of the caller's was written in place: autograd then refuses to go back
+// through what had saved it before.  (Inference tensors have no such count.)
+void written(const Tensor &x) {
+  if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
+}
+void written(PyObject *o) {  // a caller's output, or None
+  if (o != Py_None) written(THPVariable_Unpack(o));
+}
+
 void *ptr(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 // The call itself, without the interpreter's lock; its status as an exception.
@@ -175,6 +184,7 @@ PyObject *py_quantize_rows(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
   if (!call("os2_quantize_rows", lib.quantize_rows, x.m, x.k, code(X.scalar_type()), (const void *)x.p, x.ld,
             (int8_t *)ptr(q), ldq, (float *)ptr(scale), (void *)c10::cuda::getCurrentCUDAStream(dev.index()).stream()))
     return nullptr;
+  written(a[1]), written(a[2]);
   return pair(q, scale);
   END_HANDLE_TH_ERRORS
 }
@@ -213,7 +223,9 @@ PyObject *py_i8(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
              : call("os2_i8gemm", lib.i8gemm, m, n, k, (const int8_t *)x.p, x.ld, (const float *)ptr(sa), (const int8_t *)b.p,
                     b.ld, (const float *)ptr(sb), (const float *)ptr(bias), ptr(C), ldc, code(ct), ptr(ws),
                     size_t(ws.nbytes()), (void *)stream);
-  return ok ? THPVariable_Wrap(C) : nullptr;
+  if (!ok) return nullptr;
+  written(a[6]);
+  return THPVariable_Wrap(C);
   END_HANDLE_TH_ERRORS
 }
 
@@ -313,6 +325,9 @@ struct List {
       p.push_back(x.data_ptr());
     }
   }
+  void written() const {
+    for (size_t i = 0; i < p.size(); i++) ::written(at(i, ""));
+  }
 };
 
 // adamw(params, grads, exp_avg, exp_avg_sq, exp_avg_scales, exp_avg_sq_scales, step, lr, beta1, beta2, eps, weight_decay)
@@ -348,6 +363,7 @@ PyObject *py_adamw(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
             code(g.type), q8 ? 8 : 32, lr, b1, b2, eps, wd, step,
             (void *)c10::cuda::getCurrentCUDAStream(dev.index()).stream()))
     return nullptr;
+  p.written(), m.written(), v.written(), ms.written(), vs.written();
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }

@@ -90,7 +90,8 @@ def xent_backward(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, lse: t
 
 class XentFunction(torch.autograd.Function):
     """``xent`` for autograd: XentFunction.apply(H, W, labels, ignore_index) gives
-    the losses, row by row; their mean, sum or weights are ordinary operations."""
+    the losses, row by row; their mean, sum or weights are ordinary operations.
+    The gradient has no gradient of its own: to go back through it raises."""
 
     @staticmethod
     def forward(ctx, H, W, labels, ignore_index=-100):
@@ -102,9 +103,24 @@ class XentFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad):
         H, W, labels, lse = ctx.saved_tensors
-        dh, dw = xent_backward(H, W, labels, lse, grad.float(), ctx.ignore_index,
-                               ctx.needs_input_grad[0], ctx.needs_input_grad[1])
+        # (with create_graph only is a gradient taken while autograd records)
+        gradient = _XentGradient.apply if torch.is_grad_enabled() else xent_backward
+        dh, dw = gradient(H, W, labels, lse, grad.float(), ctx.ignore_index,
+                          ctx.needs_input_grad[0], ctx.needs_input_grad[1])
         return dh, dw, None, None
+
+
+class _XentGradient(torch.autograd.Function):
+    """``xent_backward`` where a graph of the gradient is asked for: a function of H, W
+    and grad that raises when it is differentiated, instead of a constant."""
+
+    @staticmethod
+    def forward(ctx, H, W, labels, lse, grad, ignore_index, need_dh, need_dw):
+        return xent_backward(H, W, labels, lse, grad, ignore_index, need_dh, need_dw)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("XentFunction: the gradient has no gradient of its own")
 
 
 # -------------------------------------------------------------------- AdamW

@@ -63,7 +63,7 @@ def load(build_if_missing: bool = True):
         if not os.path.exists(path):
             if not build_if_missing or path != _build.LIB:
                 raise RuntimeError(f"libos2 not built: {path} is missing")
-            _build.build()
+            _build.build_lib()
         L = ct.CDLL(path)
         i, sz, vp, d = ct.c_int, ct.c_size_t, ct.c_void_p, ct.c_void_p
         L.os2_workspace_size.argtypes = [i, i, i, i, i]

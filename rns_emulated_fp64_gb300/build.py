@@ -78,16 +78,28 @@ def _stale(outputs: str, inputs: list[str]) -> bool:
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None,
           debug: bool = False) -> str:
-    """Compile (if stale) libos2.so and the native part of head.py, and return the
-    path of libos2.so (debug: the build with the kernels' index checks, in
-    _build_debug/)."""
+    """Compile (if stale) libos2.so and the native part of head.py, side by side, and
+    return the path of libos2.so (debug: ``build_lib``'s, alone).  Where the native
+    part cannot be built, that is raised after the library is there."""
+    if debug:
+        return build_lib(force, verbose, extra, debug)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        head = ex.submit(build_head, force)
+        lib = build_lib(force, verbose, extra)
+    head.result()
+    return lib
+
+
+def build_lib(force: bool = False, verbose: bool = False, extra: list[str] | None = None,
+              debug: bool = False) -> str:
+    """Compile (if stale) and return the path of libos2.so (debug: the build with
+    the kernels' index checks, in _build_debug/).  Needs nvcc alone."""
     bdir, lib = (BUILD_DEBUG, LIB_DEBUG) if debug else (BUILD, LIB)
     os.makedirs(bdir, exist_ok=True)
     headers = [h for d, ext in ((CSRC, "*.cuh"), (CSRC, "*.h"), (os.path.join(ROOT, "include"), "*.h"))
                for h in glob.glob(os.path.join(d, ext))]
     srcs = sources()
     if not force and not _stale(lib, srcs + headers + [__file__]):
-        build_head()
         return lib
     cc = nvcc()
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -107,10 +119,8 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(os.cpu_count() or 8, len(srcs) + 1))) as ex:
-        head = ex.submit(build_head, force)
+    with ThreadPoolExecutor(max_workers=max(1, min(os.cpu_count() or 8, len(srcs)))) as ex:
         objs = list(ex.map(compile_one, srcs))
-        head.result()
     tmp = lib + f".tmp{os.getpid()}"
     r = subprocess.run([cc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"],
                        capture_output=True, text=True)

@@ -390,8 +390,8 @@ cudaError_t launch_n(int m, int n, const int8_t *c, int ldcres, const int32_t *e
   using S = Shape<N>;
   if (t->crt_tc.T != S::T || t->crt_tc.Q != S::Q || t->crt_tc.LX != S::LX)
     return cudaErrorInvalidValue;
-  static cudaError_t attr = cudaFuncSetAttribute(
-      k_crt_tc<N, OutT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::SMEM);
+  static PerDevice ready;
+  const cudaError_t attr = os2_set_smem(ready, k_crt_tc<N, OutT>, S::SMEM);
   if (attr != cudaSuccess) return attr;
   const int segs = (n + kSeg - 1) / kSeg;
   const long long rounds = (long long)m * segs;

@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <int OUT>
 cudaError_t launch_t(int m, int n, int kp, const int8_t *RA, const int8_t *RB, int b_plane_rows,
                      int N, void *out, int ldo, const Os2Tables *t, int *status, cudaStream_t s) {
-  static cudaError_t attr = cudaFuncSetAttribute(
-      k_gemm_s8<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static PerDevice ready;
+  const cudaError_t attr = os2_set_smem(ready, k_gemm_s8<OUT>, kSmem);
   if (attr != cudaSuccess) return attr;
   const dim3 grid((n + BN - 1) / BN, (m + BM - 1) / BM, N);
   k_gemm_s8<OUT><<<grid, kThreads, kSmem, s>>>(m, n, kp, RA, RB, b_plane_rows, out, ldo, t->gemm,

@@ -939,12 +939,8 @@ cudaError_t launch(int m, int n, int kp, const void *RA, const void *RB, int npl
                    const Os2Tables *t, int *status, cudaStream_t s, int b_plane_rows) {
   using C = Cfg<KIND>;
   constexpr size_t smem = 1024 + (size_t)C::STAGES * (BM + C::BN) * BK * 2 + 256;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(k_gemm_tc<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)smem);
-  });
+  static PerDevice ready;
+  const cudaError_t attr_err = os2_set_smem(ready, k_gemm_tc<KIND>, smem);
   if (attr_err != cudaSuccess) return attr_err;
   CUtensorMap ma, mb;
   if (!make_map(&ma, RA, kp, m, nplanes, BM, m) ||
@@ -976,13 +972,8 @@ template <int BOUND, int I8 = 0>
 cudaError_t set_smem2() {
   constexpr size_t smem = smem2_bytes<I8>();
   static_assert(smem <= 227 * 1024, "shared memory of the 2-SM kernel");
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(k_gemm_tc2<BOUND, I8>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  });
-  return attr_err;
+  static PerDevice ready;
+  return os2_set_smem(ready, k_gemm_tc2<BOUND, I8>, smem);
 }
 
 // int8 planes [nplanes][plane_rows][kp] bytes, of which the first `rows` rows

@@ -307,12 +307,8 @@ __global__ void __launch_bounds__(Few<NG>::threads, 1)
 template <int NG>
 cudaError_t launch(const I8Args &a, cudaStream_t s) {
   using F = Few<NG>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(k_i8few<NG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)F::smem);
-  });
+  static PerDevice ready;
+  const cudaError_t attr_err = os2_set_smem(ready, k_i8few<NG>, F::smem);
   if (attr_err != cudaSuccess) return attr_err;
   FewJob j;
   j.m = a.m;
@@ -351,17 +347,20 @@ cudaError_t launch_i8few(const I8Args &a, cudaStream_t s) {
 namespace {
 
 // Clusters of c CTAs of a kernel that run at once on the device (asked once for
-// each kernel; a handful of kernels).
+// each kernel and device; a handful of kernels).
 int resident_clusters(const void *kernel, int threads, size_t smem, int c) {
   static std::mutex mu;
   static struct {
     const void *kernel;
+    int device;
     int n[9];
-  } known[16] = {};
+  } known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
   std::lock_guard<std::mutex> g(mu);
   int i = 0;
-  while (i < 15 && known[i].kernel && known[i].kernel != kernel) i++;
-  if (known[i].kernel != kernel) known[i] = {kernel, {}};
+  while (i < 63 && known[i].kernel && !(known[i].kernel == kernel && known[i].device == dev)) i++;
+  if (known[i].kernel != kernel || known[i].device != dev) known[i] = {kernel, dev, {}};
   int &n = known[i].n[c];
   if (!n) {
     cudaLaunchAttribute attr;

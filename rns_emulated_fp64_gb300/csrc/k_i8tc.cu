@@ -465,20 +465,17 @@ I8Job plan(int m, int n, int k, int *nt) {
 
 template <int NT>
 cudaError_t launch(const I8Args &a, I8Job j, cudaStream_t s) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    using T = Threads<NT>;
-    attr_err = set_up(k_i8tc<NT>, smem_tc<NT>(), T::all,
-                      128 * T::r_misc + 256 * T::r_epi + T::conv * T::r_conv);
-  });
+  using T = Threads<NT>;
+  static PerDevice ready;
+  const cudaError_t attr_err = set_up(ready, k_i8tc<NT>, smem_tc<NT>(), T::all,
+                                      128 * T::r_misc + 256 * T::r_epi + T::conv * T::r_conv);
   if (attr_err != cudaSuccess) return attr_err;
   CUtensorMap mw, mt;
   if (!map_w(&mw, a.W, a.k, a.n, a.ldw) ||
       !make_map(&mt, a.tokens, false, a.k, a.m, a.pitch, false, NT / 2))
     return cudaErrorInvalidValue;
   i8_fill(j, a);
-  return launch_after(k_i8tc<NT>, 2 * j.workers, Threads<NT>::all, smem_tc<NT>(), s, mw, mt, j,
+  return launch_after(k_i8tc<NT>, 2 * j.workers, T::all, smem_tc<NT>(), s, mw, mt, j,
                       a.status);
 }
 

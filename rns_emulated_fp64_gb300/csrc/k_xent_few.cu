@@ -281,12 +281,8 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
 template <bool BF16, int NG>
 cudaError_t launch(const XentFewArgs &a, int *parts, cudaStream_t s) {
   using S = Shape<NG>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(k_xent_few<BF16, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)S::smem);
-  });
+  static PerDevice ready;
+  const cudaError_t attr_err = os2_set_smem(ready, k_xent_few<BF16, NG>, S::smem);
   if (attr_err != cudaSuccess) return attr_err;
   Job j;
   j.v = a.v;

@@ -396,26 +396,22 @@ inline bool make_store_map(CUtensorMap *map, void *base, CUtensorMapDataType typ
 // Sets a kernel's shared memory, and checks that the block is launched with at
 // least the registers that its roles take: a larger sum would wait for ever.
 template <class K>
-cudaError_t set_up(K *kernel, size_t smem, int threads, int registers) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;
-  const cudaError_t f = cudaFuncGetAttributes(&fa, kernel);
-  if (f != cudaSuccess) return f;
-  return fa.numRegs * threads < registers ? cudaErrorInvalidConfiguration : cudaSuccess;
+cudaError_t set_up(PerDevice &ready, K *kernel, size_t smem, int threads, int registers) {
+  return os2_set_smem(ready, kernel, smem, [&]() -> cudaError_t {
+    cudaFuncAttributes fa;
+    const cudaError_t f = cudaFuncGetAttributes(&fa, kernel);
+    if (f != cudaSuccess) return f;
+    return fa.numRegs * threads < registers ? cudaErrorInvalidConfiguration : cudaSuccess;
+  });
 }
 
 template <bool BF16, bool A_MN, bool B_MN, class Epi>
 cudaError_t launch_mm2(const CUtensorMap &ma, const CUtensorMap &mb, const Job &job,
                        const Epi &epi, int *status, cudaStream_t s,
                        const CUtensorMap *md = nullptr) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = set_up(k_mm2<BF16, A_MN, B_MN, Epi>, kSmem, kThreads,
-                      128 * kRegsMisc + 256 * kRegsEpi);
-  });
+  static PerDevice ready;
+  const cudaError_t attr_err = set_up(ready, k_mm2<BF16, A_MN, B_MN, Epi>, kSmem, kThreads,
+                                      128 * kRegsMisc + 256 * kRegsEpi);
   if (attr_err != cudaSuccess) return attr_err;
   const long jobs = (long)((job.m + 2 * kHalf - 1) / (2 * kHalf)) * ((job.n + kBN - 1) / kBN) *
                     job.splits;

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "os2.h"
+#include "per_device.h"
 
 // Debug build (compiled with -DOS2_DEBUG): the kernels check the index of each
 // hand-computed global access against the extent of the array it addresses;
@@ -97,6 +98,24 @@ int *os2_status_ptr();
 
 // Number of SMs of the current device (at least 1).
 int os2_sm_count();
+
+// Sets a kernel's dynamic shared memory (its more than 48 KB) on the current device,
+// where `ready`, a static of the call's, has not seen that done; more() after it.
+template <class K, class F>
+cudaError_t os2_set_smem(PerDevice &ready, K *kernel, size_t bytes, F &&more) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return ready(dev, [&]() -> cudaError_t {
+    const cudaError_t a =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    return a != cudaSuccess ? a : more();
+  });
+}
+template <class K>
+cudaError_t os2_set_smem(PerDevice &ready, K *kernel, size_t bytes) {
+  return os2_set_smem(ready, kernel, bytes, [] { return cudaSuccess; });
+}
 
 // One CTA whose bounded mbarrier waits run out (failure-detection self-test).
 cudaError_t launch_wait_selftest(long long limit, int *status, int32_t *result, cudaStream_t s);

@@ -133,11 +133,11 @@ Tensor workspace(PyObject *o, size_t need, c10::Device dev, cudaStream_t stream)
 
 // A tensor of the caller's was written in place: autograd then refuses to go back
 // through what had saved it before.  (Inference tensors have no such count.)
-void written(const Tensor &x) {
-  if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
+void written(c10::TensorImpl *x) {
+  if (!x->is_inference()) x->bump_version();
 }
 void written(PyObject *o) {  // a caller's output, or None
-  if (o != Py_None) written(THPVariable_Unpack(o));
+  if (o != Py_None) written(THPVariable_Unpack(o).unsafeGetTensorImpl());
 }
 
 void *ptr(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
@@ -300,20 +300,23 @@ PyObject *py_xent_backward(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
 struct List {
   THPObjectPtr seq;
   std::vector<void *> p;
+  std::vector<c10::TensorImpl *> impl;  // held by seq
   at::ScalarType type = at::kFloat;
 
-  const Tensor &at(size_t i, const char *name) const { return tensor(PySequence_Fast_GET_ITEM(seq.get(), i), name); }
+  const Tensor &at(size_t i, const char *name) const { return tensor(PyTuple_GET_ITEM(seq.get(), i), name); }
   void open(PyObject *o, const char *name) {
-    seq = PySequence_Fast(o, "lists of tensors are expected");
+    // (a tuple of its own: another thread may change the caller's list during the call)
+    seq = PySequence_Tuple(o);
     if (!seq) throw python_error();
-    p.reserve(PySequence_Fast_GET_SIZE(seq.get()));
+    p.reserve(PyTuple_GET_SIZE(seq.get()));
+    impl.reserve(p.capacity());
     if (p.capacity()) type = at(0, name).scalar_type();
   }
   // sized: as large as ref's tensors, or with a value for each block of them
   void take(const List &ref, const char *name, c10::Device dev, bool type_ok, const char *types, bool blocks) {
-    const size_t count = PySequence_Fast_GET_SIZE(ref.seq.get());
-    TORCH_CHECK_VALUE(size_t(PySequence_Fast_GET_SIZE(seq.get())) == count, name, ": ",
-                      PySequence_Fast_GET_SIZE(seq.get()), " tensors for ", count, " parameters");
+    const size_t count = PyTuple_GET_SIZE(ref.seq.get());
+    TORCH_CHECK_VALUE(size_t(PyTuple_GET_SIZE(seq.get())) == count, name, ": ",
+                      PyTuple_GET_SIZE(seq.get()), " tensors for ", count, " parameters");
     TORCH_CHECK_VALUE(type_ok, name, " must be all ", types);
     for (size_t i = 0; i < count; i++) {
       const Tensor &x = at(i, name), &r = ref.at(i, "params");
@@ -323,10 +326,11 @@ struct List {
                         name, " must be contiguous, on one CUDA device, and ",
                         blocks ? "one value for each block of elements" : "of the parameters' shapes");
       p.push_back(x.data_ptr());
+      impl.push_back(x.unsafeGetTensorImpl());
     }
   }
   void written() const {
-    for (size_t i = 0; i < p.size(); i++) ::written(at(i, ""));
+    for (c10::TensorImpl *x : impl) ::written(x);
   }
 };
 
@@ -335,7 +339,7 @@ PyObject *py_adamw(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
   OS2_ARGS(12)
   List p, g, m, v, ms, vs;
   p.open(a[0], "params");
-  const size_t count = PySequence_Fast_GET_SIZE(p.seq.get());
+  const size_t count = PyTuple_GET_SIZE(p.seq.get());
   if (!count) Py_RETURN_NONE;
   as_int(int64_t(count), "params");
   const c10::Device dev = p.at(0, "params").device();

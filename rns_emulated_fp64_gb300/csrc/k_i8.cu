@@ -210,7 +210,9 @@ __global__ void __launch_bounds__(kQThreads)
 // (5.5 TB/s read and written).
 __global__ void __launch_bounds__(256)
     k_align_rows(int n, int k, const int8_t *B, long ldb, int8_t *dst, long pitch) {
-  next_may_start();  // (beside the kernel that quantises the tokens: they share nothing)
+  // (beside the kernel that quantises the tokens: they share nothing, and B, an input of
+  // the call, is complete since that one passed start_call)
+  next_may_start();
   const long per = pitch / 16, total = per * n;
   for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
     const long r = i / per;

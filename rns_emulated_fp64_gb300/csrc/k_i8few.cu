@@ -20,10 +20,11 @@
 // through global memory, with stages dealt out evenly over single CTAs, took 3 us
 // longer: 12.5 us instead of 8 for 4096 x 4096 and one token.)
 //
-// Warps: 8 or 16 as above, one more for TMA.  The first weights are asked for before
-// the kernel waits for the one in front of it on the stream, which quantises the
-// tokens: they are inputs of the call, and nothing in front of that kernel can be
-// writing them still.  Every wait is bounded, as in mm2.cuh.
+// Warps: 8 or 16 as above, one more for TMA.  The first weights are asked for, and the
+// channels' scales and bias read, before the kernel waits for the one in front of it on the
+// stream, which quantises the tokens: they are inputs of the call, and nothing in front
+// of that kernel can be writing them still (start_call).  Every wait is bounded, as in
+// mm2.cuh.
 //
 // Measured with the quantising launch: one token 7.6 us for 4096 x 4096 weights, 16.4
 // for 14336 x 4096 and 16.8 for 32000 x 2048 (3.9 TB/s; a kernel that only reads takes 6.2,

@@ -73,6 +73,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Threads<NT>::all, 1)
            const I8Job j, int *status) {
   using T = Threads<NT>;
   constexpr int RAW = raw_stages<NT>();
+  // Two groups take the stages in turn, so that with an odd number of slots a group meets
+  // every second phase of a slot's barrier only, and these have the same parity.  No wait
+  // passes on an old one all the same: MMAs end in order, and a group that comes to stage j has
+  // seen that of stage j - 2 - kTc end, so that the stages up to it were there and read.  The
+  // phase between is among them in both rings:
+  static_assert(T::groups == 1 || (RAW >= kTc + T::groups && kTc >= T::groups), "rings");
   constexpr uint32_t IDESC = idesc_f16_f32(2 * kHalf, NT);
   constexpr uint32_t TOK = 2 * tok_block<NT>();
   constexpr int COLS = NT / 2;                    // columns of an epilogue thread

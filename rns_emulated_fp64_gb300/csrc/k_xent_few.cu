@@ -105,8 +105,9 @@ __global__ void __launch_bounds__(kThreadsFew, 1)
         mbar_arrive_expect_tx(&full[st], S::stage);
         tma_load_3d(smem + st * S::stage, &mapW, &full[st], ks * kBK, t * 128, 0);
       };
-      // the first turn of the ring: W, an input of the call; then, once the kernel in
-      // front has packed them, H's rows
+      // the first turn of the ring: W, an input of the call (complete since the kernel in
+      // front passed start_call; a copy of W is waited for: overlap is off); then, once the
+      // kernel in front has packed them, H's rows
       int i = 0;
       for (int t = first; t < j.tiles && i < S::stages; t += j.clusters)
         for (int ks = s0; ks < s1 && i < S::stages; ks++) weights(i++, t, ks);

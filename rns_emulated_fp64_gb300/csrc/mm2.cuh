@@ -148,7 +148,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
 
-  // the next launch may start once all this one reads is there: a `beside` one relies on it
+  // The next launch may start once all this one reads is there: a `beside` one, which reads
+  // the same operands' kernel's output without waiting, relies on it.
   if (!job.beside) wait_for_previous();
   next_may_start();
   // counts known on the device only, never above the host's

@@ -85,7 +85,12 @@ __device__ __forceinline__ void wait_for_previous() {
 
 // A call's first kernel: launched while the kernel in front of it ends, it waits
 // for that before it does anything, and before it lets the next one begin, which may
-// then count on all that lies before the call.
+// then count on all that lies before the call.  Some do, and read the call's inputs
+// before they wait themselves: k_i8few and k_xent_few their weights (not a copy of
+// them), k_i8few its channels' scales and bias, k_align_rows the rows that it copies.
+// So in every kernel that can stand in front of one of those, next_may_start comes after
+// wait_for_previous or after a kernel of the same call in which it did; and in a
+// product (mm2.cuh) in front of a `beside` one, after its wait.
 __device__ __forceinline__ void start_call() {
   wait_for_previous();
   next_may_start();
@@ -272,10 +277,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
-// The same where no generic-proxy memory is handed over, only tensor memory
-// (ordered by tcgen05.wait and the tcgen05 fences) or the right to reuse a
-// buffer: without the release at cluster scope, whose fence costs the arriving
-// thread the better part of a microsecond.
+// The same without the release at cluster scope, whose fence costs the arriving
+// thread the better part of a microsecond.  Enough for handing over
+//  - tensor memory (ordered by tcgen05.wait and the tcgen05 fences),
+//  - the right to reuse a buffer,
+//  - what this thread wrote to shared memory of its own CTA for the tensor cores
+//    alone (k_i8tc's widened weights), after fence_async_smem: the proxy fence has
+//    made the writes visible to the async proxy before the arrival is made, and
+//    each CTA's tensor core reads them there, through that proxy, for an MMA
+//    that is issued after the arrival was seen.
+// Not for memory that a thread of the other CTA reads by ordinary loads.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

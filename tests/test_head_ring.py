@@ -85,6 +85,71 @@ def test_the_ring_of_the_kernel(tmp_path):
         every(slots, groups)
 
 
+def follow_widening(raw, slots, groups, total, late_copy, late_mma):
+    """The two rings of the product of more tokens: `raw` slots of 8-bit weights, which
+    the groups in turn widen into `slots` others, which the MMAs read in order."""
+    rfull, rempty, full, empty = [0] * raw, [0] * raw, [0] * slots, [0] * slots
+    issued, landed, mma, done = 0, set(), 0, 0
+    at, taken = [0] * groups, [False] * groups
+    passes = lambda have, phase: have % 2 != phase % 2  # noqa: E731
+
+    def advance(copy, held):
+        nonlocal issued, mma, done
+        moved = False
+        if issued < total and (issued < raw or passes(rempty[issued % raw], issued // raw - 1)):
+            issued += 1
+            moved = True
+        for i in range(issued):
+            if i not in landed and i != copy:
+                landed.add(i)
+                rfull[i % raw] += 1
+                moved = True
+        for g in range(groups):
+            j = at[g]
+            if j >= total:
+                continue
+            if j % groups != g:
+                at[g] += 1
+                moved = True
+            elif not taken[g] and passes(rfull[j % raw], j // raw):
+                if j not in landed:
+                    raise Early
+                rempty[j % raw] += 1
+                taken[g] = moved = True
+            elif taken[g] and (j < slots or passes(empty[j % slots], j // slots - 1)):
+                if j >= slots and done < j - slots + 1:
+                    raise Early
+                full[j % slots] += 1
+                at[g], taken[g] = j + 1, False
+                moved = True
+        if mma < total and passes(full[mma % slots], mma // slots):
+            mma += 1
+            moved = True
+        if done < mma and done != held:
+            empty[done % slots] += 1
+            done += 1
+            moved = True
+        return moved
+
+    for hold in ((late_copy, late_mma), (None, late_mma), (None, None)):
+        while advance(*hold):
+            pass
+    assert done == total and min(at) == total
+
+
+def test_two_groups_that_widen_in_turn():
+    def every(raw, slots, groups):
+        for late in range(4 * raw):
+            for held in [None] + list(range(0, 4 * raw, 3)):
+                follow_widening(raw, slots, groups, 6 * raw, late, held)
+
+    for raw in (5, 6, 7):                     # the kernel's: 6 for 64 tokens a tile, 5 for 128
+        every(raw, 3, 2)
+    every(4, 3, 1)
+    with pytest.raises(Early):
+        every(3, 3, 2)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("m", [1, 8, 9, 16])
 @pytest.mark.parametrize("k", [2048, 5000])

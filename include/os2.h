@@ -429,10 +429,12 @@ os2_status os2_i8linear(int m, int n, int k, int dtype, const void *X, int ldx, 
                         int ldb, const float *b_scale, const float *bias, void *C, int ldc,
                         int out_dtype, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Device workspace of os2_xent (backward = 0) and os2_xent_backward (1): the
- * packed rows of H and, in the backward pass, one piece of the logits'
- * gradients, twice (at most 256 MB each, or 2048 columns).  0 on bad args; W and ldw as in
- * the call (their alignment decides; W is not read).  256-byte aligned. */
+/* Device workspace of os2_xent (backward = 0) and os2_xent_backward (1, or
+ * OS2_XENT_BACKWARD_BF16, which is enough where dtype is OS2_BF16): the packed rows of
+ * H and, in the backward pass, one piece of the logits' gradients (at most 256 MB, or
+ * 2048 columns; in FP16 twice).  0 on bad args; W and ldw as in the call (their
+ * alignment decides; W is not read).  256-byte aligned. */
+#define OS2_XENT_BACKWARD_BF16 2
 size_t os2_xent_workspace_size(int n, int k, int v, const void *W, int ldw, int backward);
 
 /* Softmax cross entropy of the logits z = H W^T, which are never in memory:

@@ -658,13 +658,17 @@ int dh_splits(long npad, int k, int vc, int pieces) {
   return best;
 }
 
+// D is there once, in FP16 twice (kSpread).
+constexpr int d_layers(bool bf16) { return bf16 ? 1 : 2; }
+
 struct Layout {
   long npad, kp;
   int parts, vc, pieces, splits;
   size_t count, rowmap, label, zlabel, part, Hc, Wc, lse_c, grad_c, scale, d, acc, total;
 };
 
-Layout layout(int n, int k, int v, const void *W, int ldw, bool backward) {
+// layers: of D in the backward pass, 0 in the forward one.
+Layout layout(int n, int k, int v, const void *W, int ldw, int layers) {
   Layout L = {};
   L.npad = (long)os2_round_up((size_t)n, 256);
   L.kp = (long)os2_round_up((size_t)k, 64);
@@ -682,11 +686,11 @@ Layout layout(int n, int k, int v, const void *W, int ldw, bool backward) {
   L.label = take((size_t)n * 4);
   L.Hc = take((size_t)L.npad * L.kp * 2);
   if (!tma_rows(W, ldw)) L.Wc = take((size_t)v * L.kp * 2);
-  if (backward) {
+  if (layers) {
     L.lse_c = take((size_t)n * 4);
     L.grad_c = take((size_t)n * 4);
     L.scale = take(12);
-    L.d = take((size_t)L.npad * L.vc * 2 * 2);  // the second layer is FP16's
+    L.d = take((size_t)L.npad * L.vc * 2 * layers);
     L.splits = dh_splits(L.npad, k, std::min(L.vc, v), L.pieces);
     if (L.pieces * L.splits > 1)
       L.acc = take((size_t)L.splits * L.npad * os2_round_up((size_t)k, 256) * 4);
@@ -774,7 +778,7 @@ cudaError_t backward(Prep p, const uint16_t *W, long ldw, uint16_t *dW, long ldd
   uint16_t *d = at<uint16_t>(ws, L.d);
   float *acc = at<float>(ws, L.acc);
   const long acc_pitch = (long)os2_round_up((size_t)p.k, 256);
-  const int layers = BF16 ? 1 : 2;
+  const int layers = d_layers(BF16);
   const int *spread = !BF16 && p.dH ? p.spread : nullptr;
   CUtensorMap mh, mht, mw, mwt, md, mdt, mds, msum;
   const CUtensorMapDataType type =
@@ -858,7 +862,7 @@ extern "C" size_t os2_xent_workspace_size(int n, int k, int v, const void *W, in
                                           int backward) {
   if (n < 0 || k < 1 || v < 1 || ldw < k || n > kMaxRows || v > kMaxRows || k >= (1 << 24))
     return 0;
-  return layout(n, k, v, W, ldw, backward != 0).total;
+  return layout(n, k, v, W, ldw, backward ? d_layers(backward == OS2_XENT_BACKWARD_BF16) : 0).total;
 }
 
 extern "C" os2_status os2_xent(int n, int k, int v, int dtype, const void *H, int ldh,
@@ -869,7 +873,7 @@ extern "C" os2_status os2_xent(int n, int k, int v, int dtype, const void *H, in
   if (st) return st;
   if (n == 0) return OS2_OK;
   if (!loss || !lse || !aligned(loss, 4) || !aligned(lse, 4)) return OS2_ERR_INVALID_ARG;
-  const Layout L = layout(n, k, v, W, ldw, false);
+  const Layout L = layout(n, k, v, W, ldw, 0);
   if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256))
     return OS2_ERR_WORKSPACE;
   Prep p = {};
@@ -909,7 +913,7 @@ extern "C" os2_status os2_xent_backward(int n, int k, int v, int dtype, const vo
                ? OS2_OK
                : OS2_ERR_CUDA;
   }
-  const Layout L = layout(n, k, v, W, ldw, true);
+  const Layout L = layout(n, k, v, W, ldw, d_layers(dtype == OS2_BF16));
   if (!workspace || workspace_bytes < L.total || !aligned(workspace, 256))
     return OS2_ERR_WORKSPACE;
   Prep p = {};

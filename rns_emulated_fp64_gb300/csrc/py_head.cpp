@@ -287,7 +287,7 @@ PyObject *py_xent_backward(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
   const Tensor y = vec(a[2], "labels", n, at::kLong, t.dev), lse = vec(a[3], "lse", n, at::kFloat, t.dev),
                grad = vec(a[4], "grad", n, at::kFloat, t.dev);
   const Tensor dh = need_dh ? fresh({n, k}, dt, t.dev) : Tensor(), dw = need_dw ? fresh({v, k}, dt, t.dev) : Tensor();
-  const Tensor ws = workspace(a[8], lib.xent_workspace(n, k, v, t.w.p, t.w.ld, 1), t.dev, stream);
+  const Tensor ws = workspace(a[8], lib.xent_workspace(n, k, v, t.w.p, t.w.ld, t.dtype == OS2_BF16 ? OS2_XENT_BACKWARD_BF16 : 1), t.dev, stream);
   if (!call("os2_xent_backward", lib.xent_backward, n, k, v, t.dtype, (const void *)t.h.p, t.h.ld, (const void *)t.w.p,
             t.w.ld, (const long long *)ptr(y), integer(a[5]), (const float *)ptr(lse), (const float *)ptr(grad), ptr(dh), k,
             ptr(dw), k, ptr(ws), size_t(ws.nbytes()), (void *)stream))

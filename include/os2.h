@@ -443,7 +443,8 @@ size_t os2_xent_workspace_size(int n, int k, int v, const void *W, int ldw, int 
  * OS2_ERR_UNSUPPORTED), ldh, ldw >= k; labels: n int64.  Rows whose label is
  * ignore_index have loss 0 and lse 0 and are not computed.  Any other label
  * outside [0, v) sets OS2_ERR_RANGE in the status word and counts as ignored.
- * Sums and exponentials are FP32.  k >= 1, v >= 1; n, v <= 2^22, k < 2^24
+ * Sums and exponentials are FP32.  A logit of NaN or +Inf makes its row's loss and lse
+ * NaN, one of -Inf is a term of 0.  k >= 1, v >= 1; n, v <= 2^22, k < 2^24
  * (else OS2_ERR_UNSUPPORTED). */
 os2_status os2_xent(int n, int k, int v, int dtype, const void *H, int ldh, const void *W, int ldw,
                     const long long *labels, long long ignore_index, float *loss, float *lse,

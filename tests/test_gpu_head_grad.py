@@ -95,3 +95,23 @@ def test_dh_of_rows_far_apart_in_f16(n, k, v, least, most):
     only, none = os2.xent_backward(h, w, y, lse, grad, need_dw=False)
     none2, only_w = os2.xent_backward(h, w, y, lse, grad, need_dh=False)
     assert none is None and none2 is None and torch.equal(only, dh) and torch.equal(only_w, dw)
+
+
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("k", [64, 1100])
+def test_logits_that_are_infinite(n, k):
+    """A logit of -Inf is a term of 0; one of +Inf makes its row's values NaN, and no other's."""
+    h, w, y, _ = xent_case(n, k, 700, torch.bfloat16, 0.0, 41)
+    h[:, 5] = 1.0
+    y = y.clamp(min=10)
+    w2 = w.clone()
+    w2[7, 5] = -float("inf")
+    loss, lse = os2.xent(h, w2, y)
+    (want, want_lse, _, _), (tl, ts, _, _) = xent_want(h, torch.cat([w[:7], w[8:]]), y - 1, torch.ones(n, device="cuda"))
+    close(loss, want, tl)
+    close(lse, want_lse, ts)
+    h[1, 5] = -1.0                                # a logit of +Inf for this row alone
+    base = os2.xent(h, w2, y)
+    for got, before in zip(base, (loss, lse)):
+        rest = torch.arange(n, device="cuda") != 1
+        assert torch.isnan(got[1]) and torch.equal(got[rest], before[rest])

@@ -25,17 +25,19 @@ ADAMW_BLOCK = 256  # elements that share a scale of an 8-bit moment
 
 def _run(f, stream, like, *args):
     """The call; what it allocates and copies belongs to its stream."""
-    if stream is None:
+    if stream is None or not hasattr(like, "get_device"):  # (no tensor: nothing to do, or f's error)
         return f(*args)
+    index = like.get_device()
+    if index < 0:
+        raise ValueError("every tensor must be on one CUDA device")
     if not isinstance(stream, torch.cuda.Stream):
-        index = like.get_device()
-        if index < 0:
-            raise ValueError("every tensor must be on one CUDA device")
         # The default stream has the handles 0 and 1 (the legacy one), neither of which
         # ExternalStream takes for it.
         handle = int(stream)
         stream = (torch.cuda.default_stream(index) if handle in (0, 1)
                   else torch.cuda.ExternalStream(handle, device=index))
+    elif stream.device_index != index:
+        raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
     with torch.cuda.stream(stream):
         return f(*args)
 

@@ -8,15 +8,37 @@ import rns_emulated_fp64_gb300 as os2
 from rns_emulated_fp64_gb300 import head
 
 
+class OnDevice:
+    def get_device(self):
+        return 0
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """Its device's current stream would be the call's, not the tensors'."""
+    class Stream:
+        def __init__(self, index):
+            self.device_index = index
+
+    seen = []
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: seen.append(s) or contextlib.nullcontext())
+    assert head._run(lambda: 3, Stream(0), OnDevice()) == 3 and len(seen) == 1
+    with pytest.raises(ValueError, match="cuda:1"):
+        head._run(lambda: 3, Stream(1), OnDevice())
+    with pytest.raises(ValueError, match="one CUDA device"):
+        head._run(lambda: 3, Stream(0), torch.zeros(2))
+    assert len(seen) == 1
+    for stream in (Stream(0), 0):                 # what is no tensor is the call's to refuse
+        os2.adamw([], [], [], [], step=1, lr=1e-3, stream=stream)
+        with pytest.raises(ValueError, match="must be a tensor"):
+            os2.quantize_rows([1.0], stream=stream)
+
+
 def test_the_default_streams_handles(monkeypatch):
     seen = []
     monkeypatch.setattr(torch.cuda, "default_stream", lambda device: ("default", device))
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda ptr, device: ("external", ptr, device))
     monkeypatch.setattr(torch.cuda, "stream", lambda s: seen.append(s) or contextlib.nullcontext())
-
-    class OnDevice:
-        def get_device(self):
-            return 0
 
     for stream in (0, 1, 2, 0x7F0010):
         assert head._run(lambda x: x, stream, OnDevice(), 5) == 5

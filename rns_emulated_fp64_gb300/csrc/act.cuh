@@ -5,6 +5,9 @@
 //              reciprocal and five multiply-adds; relu, silu = z s(z), s(z) = 1 / (1 + e^-z)
 //   gelu_tanh  z (1 + tanh u) / 2 = z s(2 u),  u = sqrt(2 / pi) (z + 0.044715 z^3)
 #pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
 #include "os2_internal.cuh"
 
 namespace os2act {
@@ -59,7 +62,22 @@ __device__ __forceinline__ void values(float (&z)[N], int act) {
   }
 }
 
-// d <- d act'(z).
+// z held to [-100, 100], two 16-bit entries at once: a slope is 0 or 1 in FP32 from far less on, and
+// beyond it z^3 would overflow, or an infinite z (a rounded one, in FP16 from 65520 on) meet a zero.
+// NaN stays.  (In FP32, entry by entry, a gradient of eight tokens took 23.5 us in place of 23.1.)
+template <bool BF16>
+__device__ __forceinline__ uint32_t near0(uint32_t z) {
+  if (BF16) {
+    const __nv_bfloat162 far = __bfloat162bfloat162(__float2bfloat16_rn(100.f)), x = reinterpret_cast<const __nv_bfloat162 &>(z),
+                         y = __hmax2_nan(__hmin2_nan(x, far), __hneg2(far));
+    return reinterpret_cast<const uint32_t &>(y);
+  }
+  const __half2 far = __half2half2(__float2half_rn(100.f)), x = reinterpret_cast<const __half2 &>(z),
+                y = __hmax2_nan(__hmin2_nan(x, far), __hneg2(far));
+  return reinterpret_cast<const uint32_t &>(y);
+}
+
+// d <- d act'(z), z as near0 gives it.
 template <int N>
 __device__ __forceinline__ void slopes(float (&d)[N], const float (&z)[N], int act) {
   switch (act) {

@@ -106,17 +106,27 @@ Tensor out_rows(PyObject *o, const char *name, int64_t m, int64_t n, at::ScalarT
   return x;
 }
 
+// Where a matrix (or a vector, as one row) lies: m rows of `row` bytes, `pitch` apart.
+struct Area {
+  intptr_t p;
+  int64_t m, row, pitch;
+  Area(const Rows &x, size_t elem) : p((intptr_t)x.p), m(x.m), row(x.k * (int64_t)elem), pitch(x.ld * (int64_t)elem) {}
+  Area(const Tensor &x, int ld) : Area(Rows{int(x.size(0)), int(x.size(1)), ld, x.data_ptr()}, x.element_size()) {}
+  explicit Area(const Tensor &v) : p(v.defined() ? (intptr_t)v.data_ptr() : 0), m(1), row(p ? int64_t(v.nbytes()) : 0), pitch(row) {}
+};
+
 // Refuses an output of the caller's that shares memory with `in`; where they are the same entry
 // on entry, it may (same).
-void apart(const Tensor &out, const char *name, int ld, const Rows &in, const char *other, size_t elem, bool same = false) {
-  const int64_t m = out.size(0), n = out.size(1), e = out.element_size();
-  if (!in.p || !m || !n || !in.m || !in.k) return;
-  const intptr_t p = (intptr_t)out.data_ptr(), q = (intptr_t)in.p, row = ld * e, row_in = in.ld * (int64_t)elem;
-  if (p + (m - 1) * row + n * e <= q || q + (in.m - 1) * row_in + in.k * (int64_t)elem <= p) return;
-  if (same && p == q && (row == row_in || m == 1) && e == (int64_t)elem) return;
-  if (row == row_in) {  // side by side in rows of one length
-    const intptr_t off = ((q - p) % row + row) % row;
-    if (off >= n * e && off + in.k * (int64_t)elem <= row) return;
+void apart(const Area &out, const char *name, const Area &in, const char *other, bool same = false) {
+  if (!out.p || !in.p || !out.m || !in.m || !out.row || !in.row) return;
+  if (out.p + (out.m - 1) * out.pitch + out.row <= in.p || in.p + (in.m - 1) * in.pitch + in.row <= out.p) return;
+  // (one row has any pitch)
+  const int64_t pitch = out.m > 1 ? out.pitch : in.pitch;
+  if (out.m == 1 || in.m == 1 || out.pitch == in.pitch) {
+    if (same && out.p == in.p && out.m == in.m && out.row == in.row) return;
+    // side by side in rows of one length
+    const int64_t off = ((in.p - out.p) % pitch + pitch) % pitch;
+    if (off >= out.row && off + in.row <= pitch) return;
   }
   TORCH_CHECK_VALUE(false, name, " must not overlap ", other);
 }
@@ -457,14 +467,24 @@ PyObject *py_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
   const Tensor h = a[2] == Py_None ? Tensor() : out_rows(a[5], "out_h", x.m, x.k, t, dev, ldh);
   const Tensor scale = q8 ? out_vec(a[6], "scale", x.m, at::kFloat, dev) : Tensor();
   const size_t e = X.element_size();
-  if (a[4] != Py_None) {
-    apart(y, "out", ldy, x, "X", e, !q8);
-    apart(y, "out", ldy, r, "residual", e, !q8);
-  }
-  if (h.defined() && a[5] != Py_None) {
-    apart(h, "out_h", ldh, x, "X", e, true);
-    apart(h, "out_h", ldh, r, "residual", e, true);
-    if (a[4] != Py_None) apart(y, "out", ldy, Rows{x.m, x.k, ldh, ptr(h)}, "out_h", e);
+  const bool own_y = a[4] != Py_None, own_h = h.defined() && a[5] != Py_None, own_s = q8 && a[6] != Py_None;
+  if (own_y || own_h || own_s) {
+    const Area ax(x, e), ar(r, e), aw(w), as(own_s ? scale : Tensor()), ah = own_h ? Area(h, ldh) : Area(Tensor());
+    if (own_y) {
+      const Area ay(y, ldy);
+      apart(ay, "out", ax, "X", !q8);
+      apart(ay, "out", ar, "residual", !q8);
+      apart(ay, "out", aw, "weight");
+      apart(ay, "out", ah, "out_h");
+      apart(as, "scale", ay, "out");
+    }
+    apart(ah, "out_h", ax, "X", true);
+    apart(ah, "out_h", ar, "residual", true);
+    apart(ah, "out_h", aw, "weight");
+    apart(as, "scale", ax, "X");
+    apart(as, "scale", ar, "residual");
+    apart(as, "scale", aw, "weight");
+    apart(as, "scale", ah, "out_h");
   }
   void *const stream = (void *)c10::cuda::getCurrentCUDAStream(dev.index()).stream();
   const bool ok =
@@ -561,9 +581,11 @@ PyObject *py_linear(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
   int ldy;
   const Tensor Y = out_rows(a[6], "out", m, n, t, dev, ldy), pre = a[5] == Py_True ? fresh({m, n}, t, dev) : Tensor();
   if (a[6] != Py_None) {
-    apart(Y, "out", ldy, x, "X", 2);
-    apart(Y, "out", ldy, w, "W", 2);
-    apart(Y, "out", ldy, r, "residual", 2, true);
+    const Area y(Y, ldy);
+    apart(y, "out", Area(x, 2), "X");
+    apart(y, "out", Area(w, 2), "W");
+    apart(y, "out", Area(r, 2), "residual", true);
+    apart(y, "out", Area(bias), "bias");
   }
   const Tensor ws = workspace(a[7], lib.linear_workspace(m, n, k, x.p, x.ld, w.p, w.ld), dev, stream);
   if (!call("os2_linear", lib.linear, m, n, k, code(t), (const void *)x.p, x.ld, (const void *)w.p, w.ld, (const void *)ptr(bias),

@@ -10,7 +10,11 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
 
+#include <ATen/Context.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <ATen/ops/empty.h>
+#include <ATen/record_function.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -88,8 +92,13 @@ Tensor vec(PyObject *o, const char *name, int64_t n, at::ScalarType t, c10::Devi
   return x.is_contiguous() ? x : x.contiguous();
 }
 
-// (past the dispatcher, which takes 0.4 us: a norm with a residual of one row 5.4 and 4.4 us a call)
+// A new output: past the dispatcher, which takes 0.4 us (a norm with a residual of one row 5.4 and
+// 4.5 us a call, 0.1 of it these questions), unless someone looks on there: a dispatch mode, a profiler, or the filling
+// of new memory that deterministic algorithms ask for.
 Tensor fresh(at::IntArrayRef shape, at::ScalarType t, c10::Device dev) {
+  if (c10::impl::TorchDispatchModeTLS::any_modes_set() || at::hasCallbacks() ||
+      (at::globalContext().deterministicAlgorithms() && at::globalContext().deterministicFillUninitializedMemory()))
+    return at::empty(shape, at::TensorOptions().dtype(t).device(dev));
   return at::detail::empty_cuda(shape, t, dev, std::nullopt);
 }
 
@@ -157,12 +166,14 @@ Tensor workspace(PyObject *o, size_t need, c10::Device dev, cudaStream_t stream)
     TORCH_CHECK_VALUE(x.device() == dev && x.is_contiguous(), "workspace must be contiguous and on ", dev);
     return x;
   }
+  // (nobody's but the kernels': a mode that makes stand-ins of new tensors would have one kept)
+  auto scratch = [&](size_t bytes) { return at::detail::empty_cuda({int64_t(bytes)}, at::kByte, dev, std::nullopt); };
   if (need > kKeep || c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
-    return fresh({int64_t(need)}, at::kByte, dev);
+    return scratch(need);
   static thread_local Kept kept;
   Tensor &ws = kept[{dev.index(), stream}];
   if (!ws.defined() || size_t(ws.numel()) < need)
-    ws = fresh({int64_t(std::min(kKeep, std::max(size_t(1) << 20, 2 * need)))}, at::kByte, dev);
+    ws = scratch(std::min(kKeep, std::max(size_t(1) << 20, 2 * need)));
   return ws;
 }
 

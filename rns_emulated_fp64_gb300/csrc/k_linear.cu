@@ -222,9 +222,11 @@ __global__ void __launch_bounds__(64 * kSlopeRows) k_linear_prepare(const Slope 
         return make_uint4(w[0], w[1], w[2], w[3]);
       };
       g = take(p.dY + (size_t)row * p.lddy + col);
-      if (p.act != OS2_ACT_NONE) z = take(p.pre + (size_t)row * p.ldp + col);
-      const uint32_t gw[4] = {g.x, g.y, g.z, g.w},
-                     zw[4] = {os2act::near0<BF16>(z.x), os2act::near0<BF16>(z.y), os2act::near0<BF16>(z.z), os2act::near0<BF16>(z.w)};
+      if (p.act != OS2_ACT_NONE) {
+        z = take(p.pre + (size_t)row * p.ldp + col);
+        z = make_uint4(os2act::near0<BF16>(z.x), os2act::near0<BF16>(z.y), os2act::near0<BF16>(z.z), os2act::near0<BF16>(z.w));
+      }
+      const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, zw[4] = {z.x, z.y, z.z, z.w};
       float d[8], at[8];
 #pragma unroll
       for (int i = 0; i < 8; i++) {

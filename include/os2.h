@@ -581,7 +581,8 @@ os2_status os2_linear(int m, int n, int k, int dtype, const void *X, int ldx, co
 /* Its gradient, for dY the gradient of Y (and of R): D = dY act'(pre),
  *   dX = D W,   dW = D^T X,   db = sum over the rows of D,
  * dX (m x k), dW (n x k) of `dtype`, db (n values) of db_dtype (OS2_F32 or `dtype`); each may be NULL.  pre
- * is not read for OS2_ACT_NONE; where it is infinite (rounded, perhaps) act' is its limit, 1 or 0.  D is rounded to `dtype` for the products, not for db; sums
+ * is not read for OS2_ACT_NONE; where it is infinite (rounded, perhaps) act' is its limit, 1 or 0.  D is rounded to `dtype` for the products, not for db (in FP16
+ * it is held times 7/8 behind GELU and SiLU: it does not overflow where dY does not); sums
  * are FP32, results rounded once and overwritten; they do not overlap inputs. */
 size_t os2_linear_backward_workspace_size(int m, int n, int k, const void *X, int ldx,
                                           const void *W, int ldw, const void *dY, int lddy,

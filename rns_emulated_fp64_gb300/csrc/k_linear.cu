@@ -5,7 +5,9 @@
 //
 // Products on the tensor cores (mm2.cuh; few tokens: k_linear_few.cu), sums FP32; y, pre, dx,
 // dW and db are rounded once.  D is rounded to the operands' type, as an operand of the two
-// products has to be (without an activation it is dy itself); db takes it unrounded.
+// products has to be (without an activation it is dy itself); db takes it unrounded.  In FP16, D is
+// held times 7/8 where act' reaches 1.13, and dx and dW are multiplied by 8/7 before they are
+// rounded: D would overflow where dy does not.  (A half would take a bit from D's smallest numbers.)
 // Nothing is transposed in memory: W, D and x are read as they lie (MN-major operands).
 //
 // Bound by the tensor cores: 8192 x 16384 x 4096 BF16 with SiLU 555 us (1.98 PFLOP/s; in a loop, at
@@ -171,6 +173,7 @@ struct Slope {
   long lddy, ldp;
   uint16_t *D;        // or null
   long pitch;
+  float held;         // D is held times this
   float *part;        // [strips][part_pitch] sums of columns, or null
   long part_pitch;
   void *db;           // the sums themselves, where there is one strip
@@ -236,9 +239,13 @@ __global__ void __launch_bounds__(64 * kSlopeRows) k_linear_prepare(const Slope 
       os2act::slopes(d, at, p.act);
 #pragma unroll
       for (int i = 0; i < 8; i++) sum[i] += d[i];
-      if (p.D)
+      if (p.D) {
+        if (!BF16)
+#pragma unroll
+          for (int i = 0; i < 8; i++) d[i] *= p.held;
         *reinterpret_cast<uint4 *>(p.D + (size_t)row * p.pitch + col) =
             make_uint4(pack2<BF16>(d[0], d[1]), pack2<BF16>(d[2], d[3]), pack2<BF16>(d[4], d[5]), pack2<BF16>(d[6], d[7]));
+      }
     }
   if (!p.part && !p.db) return;
 #pragma unroll
@@ -256,12 +263,13 @@ __global__ void __launch_bounds__(64 * kSlopeRows) k_linear_prepare(const Slope 
   }
 }
 
-// A product's result rounded once: by TMA where its rows allow it, else by rows.
+// A product's result rounded once, in FP16 times `by` before it: by TMA where its rows allow it, else by rows.
 template <bool BF16, bool TMA>
 struct RoundEpi {
   uint16_t *out;
   long ld;
   int n;
+  float by;
   BlockSender sender = {};
 
   __device__ __forceinline__ void unit(uint32_t taddr, int row, int col0, int, bool, bool, int m, const CUtensorMap *mapD,
@@ -275,13 +283,15 @@ struct RoundEpi {
       __syncwarp();
       tmem_ld32(taddr + g * 32, r);
       tmem_wait_ld();
+      float z[32];
+#pragma unroll
+      for (int i = 0; i < 32; i++) z[i] = BF16 ? __uint_as_float(r[i]) : __uint_as_float(r[i]) * by;
       uint4 v[4];
 #pragma unroll
       for (int q = 0; q < 4; q++) {
         uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-          w[i] = pack2<BF16>(__uint_as_float(r[8 * q + 2 * i]), __uint_as_float(r[8 * q + 2 * i + 1]));
+        for (int i = 0; i < 4; i++) w[i] = pack2<BF16>(z[8 * q + 2 * i], z[8 * q + 2 * i + 1]);
         v[q] = make_uint4(w[0], w[1], w[2], w[3]);
       }
       if constexpr (TMA) {
@@ -313,6 +323,7 @@ struct Parts {
   void *out;
   long ld;
   bool vec, f32;
+  float by;           // in FP16, the sums times this
   int groups() const { return parts ? (int)std::min<long>(((cols + 3L) / 4 * rows + 255) / 256, 1 << 20) : 0; }
 };
 struct Finish {
@@ -368,6 +379,9 @@ __global__ void __launch_bounds__(256) k_linear_finish(const Finish f, int g0, i
 #pragma unroll
       for (int u = 0; u < 8; u++) x[0] += v[u].x, x[1] += v[u].y, x[2] += v[u].z, x[3] += v[u].w;
     }
+    if (!BF16)
+#pragma unroll
+      for (int q = 0; q < 4; q++) x[q] *= p.by;
     uint16_t *dst = static_cast<uint16_t *>(p.out) + row * p.ld + h;
     if (p.vec && h + 4 <= p.cols) {
       *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]));
@@ -490,7 +504,7 @@ struct Product {
 
 template <bool BF16, bool A_MN>
 cudaError_t product(const CUtensorMap &ma, const CUtensorMap &mb, const Product &p, int terms, bool beside, uint16_t *out,
-                    long ld, float *acc, int *status, cudaStream_t s) {
+                    long ld, float by, float *acc, int *status, cudaStream_t s) {
   const Job job{p.rows, p.cols, terms, nullptr, nullptr, INT_MAX, p.parts, beside};
   CUtensorMap mo;
   if (p.parts > 1) {
@@ -501,14 +515,14 @@ cudaError_t product(const CUtensorMap &ma, const CUtensorMap &mb, const Product 
   if (tma_rows(out, ld)) {
     if (!make_store_map(&mo, out, BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p.cols, p.rows, ld))
       return cudaErrorInvalidValue;
-    return launch_mm2<BF16, A_MN, true>(ma, mb, job, RoundEpi<BF16, true>{out, ld, p.cols}, status, s, &mo);
+    return launch_mm2<BF16, A_MN, true>(ma, mb, job, RoundEpi<BF16, true>{out, ld, p.cols, by}, status, s, &mo);
   }
-  return launch_mm2<BF16, A_MN, true>(ma, mb, job, RoundEpi<BF16, false>{out, ld, p.cols}, status, s);
+  return launch_mm2<BF16, A_MN, true>(ma, mb, job, RoundEpi<BF16, false>{out, ld, p.cols, by}, status, s);
 }
 
-Parts parts_of_product(const Product &p, const float *acc, void *out, long ld) {
+Parts parts_of_product(const Product &p, const float *acc, void *out, long ld, float by) {
   const long pitch = (long)os2_round_up((size_t)p.cols, 256), rows = (long)os2_round_up((size_t)p.rows, 256);
-  return {acc, p.parts > 1 ? p.parts : 0, p.rows, rows * pitch, pitch, p.cols, out, ld, tma_rows(out, ld), false};
+  return {acc, p.parts > 1 ? p.parts : 0, p.rows, rows * pitch, pitch, p.cols, out, ld, tma_rows(out, ld), false, by};
 }
 
 // --------------------------------------------------------------------- host
@@ -655,6 +669,9 @@ cudaError_t backward(LinearArgs a, const Backward &b, const uint16_t *dY, long l
   const uint16_t *D = dY;
   long ldd = lddy;
   Slope p = {};
+  const bool steep = !BF16 && a.act != OS2_ACT_NONE && a.act != OS2_ACT_RELU;
+  const float by = steep ? 8.f / 7.f : 1.f;
+  p.held = steep ? 0.875f : 1.f;
   // (not b.d: TMA takes dY, and so does k_linear_sums; by what it is given alone, so that db does not
   // depend on what else is asked for)
   const bool sums = db && !b.d && a.m <= kSumsRows;
@@ -679,7 +696,7 @@ cudaError_t backward(LinearArgs a, const Backward &b, const uint16_t *dY, long l
   if (e != cudaSuccess) return e;
   auto finish = [&](const Parts &x, const Parts &w) {
     Finish f = {{x, w, {}}};
-    if (db && !one) f.p[2] = {part, b.strips, 1, b.pitch, b.pitch, a.n, db, b.pitch, false, db_dtype == OS2_F32};
+    if (db && !one) f.p[2] = {part, b.strips, 1, b.pitch, b.pitch, a.n, db, b.pitch, false, db_dtype == OS2_F32, 1.f};
     const int most = 8 * os2_sm_count(), g0 = std::min(f.p[0].groups(), most), g1 = g0 + std::min(f.p[1].groups(), most),
               g2 = g1 + (db && !one ? (a.n + 31) / 32 : 0);
     return g2 ? launch_after(k_linear_finish<BF16>, g2, 256, 0, s, f, g0, g1, products) : cudaSuccess;
@@ -695,27 +712,28 @@ cudaError_t backward(LinearArgs a, const Backward &b, const uint16_t *dY, long l
     f.bf16 = BF16;
     f.X = D, f.ldx = ldd, f.W = a.W, f.ldw = a.ldw;
     f.Y = dX, f.ldy = lddx;
+    f.by = by;
     f.status = a.status;
     e = launch_linear_few(f, true, s);
     if (e != cudaSuccess) return e;
   } else if (dX) {
     if (!make_map(&md, D, BF16, a.n, a.m, ldd, false) || !make_map(&mw, a.W, BF16, a.k, a.n, a.ldw, true))
       return cudaErrorInvalidValue;
-    e = product<BF16, false>(md, mw, b.dx, a.n, false, dX, lddx, accx, a.status, s);
+    e = product<BF16, false>(md, mw, b.dx, a.n, false, dX, lddx, by, accx, a.status, s);
     if (e != cudaSuccess) return e;
   }
   if (dW) {
     if (!make_map(&mdt, D, BF16, a.n, a.m, ldd, true) || !make_map(&mx, a.X, BF16, a.k, a.m, a.ldx, true))
       return cudaErrorInvalidValue;
     // (dW's product reads nothing of dX's)
-    e = product<BF16, true>(mdt, mx, b.dw, a.m, dX != nullptr, dW, lddw, accw, a.status, s);
+    e = product<BF16, true>(mdt, mx, b.dw, a.m, dX != nullptr, dW, lddw, by, accw, a.status, s);
     if (e != cudaSuccess) return e;
   }
   if (sums) {
     e = add_up();
     if (e != cudaSuccess) return e;
   }
-  return finish(dX ? parts_of_product(b.dx, accx, dX, lddx) : Parts{}, dW ? parts_of_product(b.dw, accw, dW, lddw) : Parts{});
+  return finish(dX ? parts_of_product(b.dx, accx, dX, lddx, by) : Parts{}, dW ? parts_of_product(b.dw, accw, dW, lddw, by) : Parts{});
 }
 
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }

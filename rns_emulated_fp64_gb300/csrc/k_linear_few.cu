@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreadsF)
         z[2] += __uint_as_float(x[c].z), z[3] += __uint_as_float(x[c].w);
       }
 #pragma unroll
-      for (int q = 0; q < 4; q++) z[q] += bias[q];
+      for (int q = 0; q < 4; q++) z[q] = W_MN && !BF16 ? z[q] * a.by : z[q] + bias[q];
       if (a.pre && in)
         store4(a.pre + (size_t)t * a.ldp + ch, make_uint2(pack2<BF16>(z[0], z[1]), pack2<BF16>(z[2], z[3])), left, j.pwhole);
       os2act::values(z, a.act);

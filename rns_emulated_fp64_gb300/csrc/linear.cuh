@@ -15,6 +15,7 @@ struct LinearArgs {
   long ldr;
   uint16_t *Y, *pre;       // pre may be null
   long ldy, ldp;
+  float by;                // dx in FP16: the sums times this
   int *status;
 };
 

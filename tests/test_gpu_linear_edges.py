@@ -4,6 +4,7 @@ import torch
 
 import rns_emulated_fp64_gb300 as os2
 from test_gpu_head import DT, clean_status, close, gen, randn  # noqa: F401
+from test_gpu_linear import close_product, grads
 
 pytestmark = pytest.mark.gpu
 
@@ -12,8 +13,9 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 def test_slopes_of_large_and_infinite_pre_activations(act, dt):
     """A slope's limits are 1 and 0: for the largest pre, and where it was rounded to infinity.  An FP32
-    sigmoid or normal distribution there is off by a unit in the last place at most, 2^-23; D is
-    rounded to the type, which holds dy itself."""
+    sigmoid or normal distribution there is off by a unit in the last place at most, 2^-23.  D is
+    rounded to the type: BF16 holds dy itself, and so does FP16 for relu; elsewhere FP16 holds 7/8 of it
+    to 2^-11, and 8/7 of that is rounded to 2^-11 again."""
     t = DT[dt]
     ends = [1e4, 6e4, float("inf")] + ([1e15, 3e19, 1e20, 1e30, 3e38] if dt == "bf16" else [7e4])
     v = torch.tensor(ends + [-e for e in ends]).to(t).cuda()
@@ -23,11 +25,12 @@ def test_slopes_of_large_and_infinite_pre_activations(act, dt):
     x, w, dy = randn(g, m, k).to(t), torch.eye(n, k, device="cuda").to(t), randn(g, m, n).to(t)
     dx, dw, db = os2.linear_backward(x, w, dy, pre=pre, activation=act, need_db=True, db_dtype=torch.float32)
     d = torch.where(v > 0, dy.double(), 0.0)
-    close(dx[:, :n], d, 2.0 ** -22 * d.abs())             # W picks D's columns
+    held = 0.0 if dt == "bf16" or act == "relu" else 2.0 ** -11
+    close(dx[:, :n], d, (2.0 ** -22 + 2.01 * held) * d.abs() + (2.0 ** -23 if held else 0.0))  # W picks D's columns
     assert (dx[:, n:] == 0).all()
     close(db, d.sum(0), m * 2.0 ** -23 * d.abs().sum(0))
     size = d.abs().t() @ x.double().abs()
-    close(dw, d.t() @ x.double(), (2.0 ** -21 + torch.finfo(t).eps / 2) * size)
+    close(dw, d.t() @ x.double(), (2.0 ** -21 + torch.finfo(t).eps / 2 + 1.01 * held) * size + (2.0 ** -23 if held else 0.0))
 
 
 @pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
@@ -43,3 +46,34 @@ def test_slope_of_nan_is_nan(act):
     for a, b, at in zip(got, want, (2, 7, 7)):
         others = torch.arange(len(a), device="cuda") != at
         assert a[at].isnan().all() and torch.equal(a[others], b[others])
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("m,n,k", [(1, 40, 64), (5, 200, 72), (40, 129, 333), (300, 200, 136), (700, 2047, 264), (2100, 72, 64)])
+def test_gradients_of_the_largest_fp16_numbers(act, m, n, k):
+    """Where dy is FP16's largest and the slope is above 1, D is beyond FP16, and its products need not be."""
+    g = gen(m + n + k)
+    x, w = (randn(g, m, k) * 0.002).half(), (randn(g, n, k) * 0.002).half()
+    dy = torch.where(randn(g, m, n) < 0, -65504.0, 65504.0).half()
+    pre = torch.where(randn(g, m, n) < 0, 1.4, 2.4).half()
+    dx, dw, db = os2.linear_backward(x, w, dy, pre=pre, activation=act, need_db=True, db_dtype=torch.float32)
+    d, dd = grads(x, w, dy, pre, act)
+    assert act in ("none", "relu") or d.abs().max() > 71000
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+    close_product(dx, d, dd, w.double(), torch.float16)
+    close_product(dw, d.t(), dd.t() if torch.is_tensor(dd) else dd, x.double(), torch.float16)
+    size = d.abs().sum(0)
+    close(db, d.sum(0), ((m // 4 + 72) * 2.0 ** -24 + 8e-6) * size)
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_gradients_of_the_smallest_fp16_numbers(act):
+    """D among FP16's subnormal numbers is off by at most half a step of them, 8/7 of it as it is held."""
+    g = gen(7)
+    m, n, k = 33, 48, 40
+    x, w = randn(g, m, k).half(), randn(g, n, k).half()
+    dy, pre = (randn(g, m, n) * 2.0 ** -19).half(), randn(g, m, n).half()
+    dx, dw, _ = os2.linear_backward(x, w, dy, pre=pre, activation=act)
+    d, dd = grads(x, w, dy, pre, act)                    # (a whole step of slack, TINY, is in dd)
+    close_product(dx, d, dd, w.double(), torch.float16)
+    close_product(dw, d.t(), dd.t(), x.double(), torch.float16)

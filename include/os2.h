@@ -593,6 +593,20 @@ os2_status os2_linear_backward(int m, int n, int k, int dtype, const void *X, in
                                void *db, int db_dtype, void *workspace, size_t workspace_bytes,
                                void *stream);
 
+/* Which of their kernels the two calls above go through on the current device, decided by
+ * sizes alone; nothing is launched.  pre, residual: whether the call has them (0, 1); rows16: whether rows of
+ * Y, pre and R are on 16-byte boundaries.
+ *   way      0: tiles of few tokens (tokens of a tile, CTAs that share its terms: tokens, cluster),
+ *            1: tiles of 256 x 256, 2: those with the terms cut into `parts`
+ *   dx_*     the same of dX (way 2 where dx_parts > 1), dw_parts: parts of dW's terms */
+typedef struct {
+  int way, tokens, cluster, parts;
+  int dx_way, dx_tokens, dx_cluster, dx_parts;
+  int dw_parts;
+} os2_linear_ways_t;
+os2_status os2_linear_ways(int m, int n, int k, int activation, int pre, int residual, int rows16,
+                           os2_linear_ways_t *ways);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,5 +13,5 @@ from .binding import (GEMM_S8_SYNC, GEMM_SIMT, GEMM_TC, GEMM_TC_1SM, GEMM_TC_I8,
                       CRT_TC, CRT_SIMT, CRT_AUTO, scale_bounds, exponents_from_bounds,
                       gemm_exponents)
 from .head import (ACTIVATIONS, ADAMW_BLOCK, LinearFunction, RMSNormFunction, XentFunction, adamw,  # noqa: F401
-                   adamw_moments, i8gemm, i8linear, linear, linear_backward, quantize_rows, rmsnorm, rmsnorm_backward, rmsnorm_quantize,
+                   adamw_moments, i8gemm, i8linear, linear, linear_backward, linear_ways, quantize_rows, rmsnorm, rmsnorm_backward, rmsnorm_quantize,
                    sample, xent, xent_backward)

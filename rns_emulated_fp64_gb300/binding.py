@@ -36,7 +36,7 @@ EXPORTS = ("os2_workspace_size", "os2_gemm", "os2_host_workspace_size", "os2_gem
            "os2_xent_workspace_size", "os2_xent", "os2_xent_backward", "os2_adamw",
            "os2_adamw_moments", "os2_rmsnorm", "os2_rmsnorm_quantize", "os2_rmsnorm_workspace_size",
            "os2_rmsnorm_backward", "os2_sample", "os2_linear_workspace_size", "os2_linear",
-           "os2_linear_backward_workspace_size", "os2_linear_backward")
+           "os2_linear_backward_workspace_size", "os2_linear_backward", "os2_linear_ways")
 
 _lib = None
 _head = None
@@ -155,6 +155,8 @@ def load(build_if_missing: bool = True):
         L.os2_linear_backward_workspace_size.restype = sz
         L.os2_linear_backward.argtypes = [i, i, i, i, d, i, d, i, d, i, d, i, i, d, i, d, i, d, i, vp, sz, vp]
         L.os2_linear_backward.restype = i
+        L.os2_linear_ways.argtypes = [i, i, i, i, i, i, i, d]
+        L.os2_linear_ways.restype = i
         f = ct.c_float
         L.os2_sample.argtypes = [i, i, i, d, i, d, d, f, d, i, d, f, d, f, d, d, vp]
         L.os2_sample.restype = i

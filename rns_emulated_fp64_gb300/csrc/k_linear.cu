@@ -615,11 +615,10 @@ Backward backward_layout(int m, int n, int k, const void *X, long ldx, const voi
 // residual 0.7, rows that TMA does not store or take 7.  1024 tokens of 8192 x 256 with GELU 15 us
 // here and 33 there, of 1024 x 8192 43 and 22.
 enum Way { kFew, kTiles, kParts };
-Way way_of(const LinearArgs &a, const Cut &cut) {
-  if (a.m <= 16) return kFew;
-  const bool rows = tma_rows(a.Y, a.ldy) && (!a.pre || tma_rows(a.pre, a.ldp)) && (!a.R || tma_rows(a.R, a.ldr));
-  const double epi = 2.3 + (a.act != OS2_ACT_NONE ? 1.7 : 0.) + (a.pre ? 1.2 : 0.) + (a.R ? 0.7 : 0.) + (rows ? 0. : 7.);
-  const double few = linear_few_plan(a.m, a.n, a.k, a.act != OS2_ACT_NONE || a.pre).us, tiles = tiles_us(a.m, a.n, a.k, epi);
+Way way_of(int m, int n, int k, bool act, bool pre, bool residual, bool rows, const Cut &cut) {
+  if (m <= 16) return kFew;
+  const double epi = 2.3 + (act ? 1.7 : 0.) + (pre ? 1.2 : 0.) + (residual ? 0.7 : 0.) + (rows ? 0. : 7.);
+  const double few = linear_few_plan(m, n, k, act || pre).us, tiles = tiles_us(m, n, k, epi);
   if (cut.parts > 1 && cut.us < std::min(few, tiles)) return kParts;
   return few <= tiles ? kFew : kTiles;
 }
@@ -783,12 +782,27 @@ extern "C" os2_status os2_linear(int m, int n, int k, int dtype, const void *X, 
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = prepare<true>(f, a, workspace, nullptr, 0, s);  // (copies, the same for both types)
   if (e != cudaSuccess) return OS2_ERR_CUDA;
-  const Way way = way_of(a, cut);
+  const bool rows = tma_rows(a.Y, a.ldy) && (!a.pre || tma_rows(a.pre, a.ldp)) && (!a.R || tma_rows(a.R, a.ldr));
+  const Way way = way_of(m, n, k, a.act != OS2_ACT_NONE, a.pre, a.R, rows, cut);
   float *const acc = at<float>(workspace, f.total);
   if (way == kFew) e = launch_linear_few(a, false, s);
   else if (way == kTiles) e = a.bf16 ? forward<true>(a, s) : forward<false>(a, s);
   else e = a.bf16 ? in_parts<true>(a, cut.parts, acc, s) : in_parts<false>(a, cut.parts, acc, s);
   return e == cudaSuccess ? OS2_OK : OS2_ERR_CUDA;
+}
+
+extern "C" os2_status os2_linear_ways(int m, int n, int k, int activation, int pre, int residual, int rows16,
+                                     os2_linear_ways_t *ways) {
+  if (!ways || m < 1 || n < 1 || k < 1 || activation < OS2_ACT_NONE || activation > OS2_ACT_SILU) return OS2_ERR_INVALID_ARG;
+  if (m > kMaxRows || n > kMaxRows || k >= (1 << 24)) return OS2_ERR_UNSUPPORTED;
+  const bool act = activation != OS2_ACT_NONE;
+  const Cut cut = cut_of(m, n, k);
+  const Way way = way_of(m, n, k, act, pre, residual, rows16, cut);
+  const Backward b = backward_layout(m, n, k, nullptr, k, nullptr, k, nullptr, n, activation);
+  const LinearPlan y = linear_few_plan(m, n, k, act || pre), dx = linear_few_plan(m, k, n, false);
+  *ways = {way, way == kFew ? y.nt : 256, way == kFew ? y.cluster : 2, way == kParts ? cut.parts : 1,
+           b.few ? kFew : b.dx.parts > 1 ? kParts : kTiles, b.few ? dx.nt : 256, b.few ? dx.cluster : 2, b.dx.parts, b.dw.parts};
+  return OS2_OK;
 }
 
 extern "C" size_t os2_linear_backward_workspace_size(int m, int n, int k, const void *X, int ldx, const void *W, int ldw,

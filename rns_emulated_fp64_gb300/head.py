@@ -18,15 +18,17 @@ given no workspace uses one that the binding keeps for the thread and stream, if
   rmsnorm_backward, RMSNormFunction addition, its gradient, and in 8 bits as
                                     i8gemm takes its tokens
   linear, linear_backward,          a linear layer with bias, activation and residual,
-  LinearFunction                    and its gradient
+  linear_ways, LinearFunction       and its gradient
   sample                            a token from each row of logits by temperature,
                                     top-k, top-p and min-p
 """
 from __future__ import annotations
 
+import ctypes as ct
+
 import torch
 
-from .binding import load_head
+from .binding import _check, load, load_head
 
 ADAMW_BLOCK = 256  # elements that share a scale of an 8-bit moment
 
@@ -268,6 +270,18 @@ def linear_backward(X: torch.Tensor, W: torch.Tensor, dY: torch.Tensor, pre=None
     activation).  db_dtype: float32 or X's type (the default)."""
     return _run(load_head().linear_backward, stream, X, X, W, dY, pre, _activation(activation),
                 need_dx, need_dw, need_db, db_dtype, workspace)
+
+
+def linear_ways(m: int, n: int, k: int, activation: str = "none", pre: bool = False, residual: bool = False,
+                aligned: bool = True) -> dict:
+    """Which kernels ``linear`` and ``linear_backward`` go through on the current device, by sizes
+    alone (os2_linear_ways): way and dx_way are 0 for tiles of few tokens, 1 for tiles of 256 x 256, 2 for
+    those with the terms cut into parts.  Nothing is launched."""
+    names = ("way", "tokens", "cluster", "parts", "dx_way", "dx_tokens", "dx_cluster", "dx_parts", "dw_parts")
+    out = (ct.c_int * len(names))()
+    _check(load().os2_linear_ways(m, n, k, _activation(activation), bool(pre), bool(residual), bool(aligned), out),
+           "os2_linear_ways")
+    return dict(zip(names, out))
 
 
 class LinearFunction(torch.autograd.Function):

@@ -4,7 +4,7 @@ import torch
 
 import rns_emulated_fp64_gb300 as os2
 from test_gpu_head import DT, clean_status, close, gen, randn  # noqa: F401
-from test_gpu_linear import close_product, grads
+from test_gpu_linear import SHAPES, case, check, close_product, grads
 
 pytestmark = pytest.mark.gpu
 
@@ -49,7 +49,7 @@ def test_slope_of_nan_is_nan(act):
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
-@pytest.mark.parametrize("m,n,k", [(1, 40, 64), (5, 200, 72), (40, 129, 333), (300, 200, 136), (700, 2047, 264), (2100, 72, 64)])
+@pytest.mark.parametrize("m,n,k", [(1, 40, 64), (5, 200, 72), (40, 129, 333), (300, 200, 136), (700, 2047, 264), (2100, 72, 64), (40, 12000, 64)])
 def test_gradients_of_the_largest_fp16_numbers(act, m, n, k):
     """Where dy is FP16's largest and the slope is above 1, D is beyond FP16, and its products need not be."""
     g = gen(m + n + k)
@@ -77,3 +77,79 @@ def test_gradients_of_the_smallest_fp16_numbers(act):
     d, dd = grads(x, w, dy, pre, act)                    # (a whole step of slack, TINY, is in dd)
     close_product(dx, d, dd, w.double(), torch.float16)
     close_product(dw, d.t(), dd.t(), x.double(), torch.float16)
+
+
+# More tiles of 256 x 256 than an SM pair each: accumulators and store buffers go from tile to tile.
+# Columns on 16-byte boundaries leave by TMA, the others by rows.
+MANY_TILES = [(2600, 4104, 264), (2600, 4101, 264), (4200, 2568, 520), (4200, 2571, 520)]
+
+
+@pytest.mark.parametrize("m,n,k", MANY_TILES)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("act,bias,residual,pre", [("none", None, False, False), ("silu", "f32", True, False), ("gelu", "same", True, True),
+                                                   ("relu", None, False, True)])
+def test_forward_over_many_tiles(m, n, k, dt, act, bias, residual, pre):
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    ways = os2.linear_ways(m, n, k, act, pre, residual, n % 8 == 0)
+    assert ways["way"] == 1 and -(-m // 256) * -(-n // 256) > 2 * pairs
+    _, x, w, b, r = case(m, n, k, dt)
+    b = None if bias is None else b.to(DT[dt]) if bias == "same" else b
+    got = os2.linear(x, w, bias=b, residual=r if residual else None, activation=act, return_pre=pre)
+    y, z = got if pre else (got, None)
+    check(x, w, b, r if residual else None, act, y, z)
+
+
+@pytest.mark.parametrize("m,n,k", [(5000, 264, 4104), (5000, 267, 4101), (600, 4104, 4104), (600, 4104, 4101)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_gradient_over_many_tiles(m, n, k, dt, act):
+    """dX (5000 x 4104) or dW (4104 x 4104) of more tiles than SM pairs, of three to five stages each."""
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    ways = os2.linear_ways(m, n, k, act)
+    rows, parts = (m, ways["dx_parts"]) if m > n else (n, ways["dw_parts"])
+    assert parts == 1 and -(-rows // 256) * -(-k // 256) > 2 * pairs and (m < n or ways["dx_way"] == 1)
+    g, x, w, _, _ = case(m, n, k, dt)
+    dy, pre = randn(g, m, n).to(DT[dt]), (randn(g, m, n) * 1.5).to(DT[dt])
+    dx, dw, _ = os2.linear_backward(x, w, dy, pre=pre, activation=act)
+    d, dd = grads(x, w, dy, pre, act)
+    close_product(dx, d, dd, w.double(), DT[dt])
+    close_product(dw, d.t(), dd.t() if torch.is_tensor(dd) else dd, x.double(), DT[dt])
+
+
+# dX with its terms cut into 24, 6, 5, 3 and 2 parts, by clusters of two, and dW's into eight
+GRADIENT_PARTS = [(40, 12000, 64), (400, 8200, 1003), (800, 8200, 520), (600, 4100, 2000), (600, 5000, 2571), (800, 1000, 520), (2048, 8, 64)]
+
+
+@pytest.mark.parametrize("m,n,k", GRADIENT_PARTS)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_gradient_in_parts(m, n, k, dt, act):
+    g, x, w, _, _ = case(m, n, k, dt)
+    dy, pre = randn(g, m, n).to(DT[dt]), (randn(g, m, n) * 1.5).to(DT[dt])
+    dx, dw, db = os2.linear_backward(x, w, dy, pre=pre, activation=act, need_db=True, db_dtype=torch.float32)
+    d, dd = grads(x, w, dy, pre, act)
+    close_product(dx, d, dd, w.double(), DT[dt])
+    close_product(dw, d.t(), dd.t() if torch.is_tensor(dd) else dd, x.double(), DT[dt])
+    off = 2e-6 * (dy.double().abs() * (1 + pre.double().abs())).sum(0)
+    close(db, d.sum(0), (m // 4 + 72) * 2.0 ** -24 * (d.abs().sum(0) + off) + off)
+    assert torch.equal(os2.linear_backward(x, w, dy, pre=pre, activation=act, need_dw=False)[0], dx)
+    assert torch.equal(os2.linear_backward(x, w, dy, pre=pre, activation=act, need_dx=False)[1], dw)
+
+
+def test_the_tested_shapes_go_every_way():
+    """The shapes compared with 64 bits here and beside reach every kernel of the linear layer, each
+    cluster size and both ways to store."""
+    seen = set()
+    for m, n, k in SHAPES + MANY_TILES + GRADIENT_PARTS + [(600, 2000, 5000), (600, 2003, 5001)]:
+        y = os2.linear_ways(m, n, k, aligned=n % 8 == 0)
+        seen.add(("way", y["way"], n % 8 == 0 if y["way"] == 1 else None))
+        seen.add(("dx", y["dx_way"], k % 8 == 0 if y["dx_way"] == 1 else None))
+        seen.add(("dw", min(y["dw_parts"], 2), k % 8 == 0 if y["dw_parts"] == 1 else None))
+        if y["way"] == 0:
+            seen |= {("cluster", y["cluster"]), ("tokens", y["tokens"])}
+        if y["dx_way"] == 0:
+            seen.add(("dx_cluster", y["dx_cluster"]))
+    wanted = {("way", 0, None), ("way", 1, True), ("way", 1, False), ("way", 2, None), ("dx", 0, None), ("dx", 1, True), ("dx", 1, False),
+              ("dx", 2, None), ("dw", 1, True), ("dw", 1, False), ("dw", 2, None), ("tokens", 16), ("tokens", 128)}
+    wanted |= {(name, c) for name in ("cluster", "dx_cluster") for c in (1, 2, 4, 8)}
+    assert wanted <= seen, sorted(wanted - seen, key=str)

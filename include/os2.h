@@ -497,8 +497,9 @@ os2_status os2_adamw_moments(long long numel, const int8_t *exp_avg, const float
  *   h = x + r, rounded to `dtype`;   y = h rho w,  rho = (mean h^2 + eps)^(-1/2).
  * X, R, H (the sum, or NULL where it is not wanted; without R it must be NULL) and
  * Y are row-major of `dtype` (os2_dtype), weight d values of weight_dtype, which is
- * OS2_F32 or `dtype`.  Sums are FP32 (squares beyond FP32's range give rho = 0); y is
- * rounded once.  H may be X or R, Y may be X (or R, without H), entry on entry; otherwise
+ * OS2_F32 or `dtype`.  Sums are FP32 (a row of squares beyond its range has rho = 0; with eps = 0,
+ * one whose entries are all below 2^-63 loses precision, and its rho is infinite where the squares vanish);
+ * y is rounded once.  H may be X or R, Y may be X (or R, without H), entry on entry; otherwise
  * outputs do not overlap inputs.  0 <= eps < 1e30; 1 <= d <= 16384 (beyond: OS2_ERR_UNSUPPORTED).
  * Rows and weights on 16-byte boundaries are fastest; then contiguous rows of any width, or others
  * that lie alike to those boundaries in all arrays. */
@@ -522,7 +523,7 @@ size_t os2_rmsnorm_workspace_size(int n, int d);
  * that of h along the residual stream, or NULL; all of `dtype`.  With xn = h rho, a = dY w:
  *   dX = rho (a - xn mean(a xn)) + dH,  the gradient of x and of r alike,
  *   dW = sum over the rows of dY xn,    of weight_dtype,
- * sums in FP32, each result rounded once.  dX or dW may be NULL (the workspace is then
+ * sums in FP32 (where those over a row leave its range: NaN), each result rounded once.  dX or dW may be NULL (the workspace is then
  * only needed for dW); dX may be dY or dH, entry on entry.  dW does not depend on timing. */
 os2_status os2_rmsnorm_backward(int n, int d, int dtype, const void *H, int ldh, const void *weight,
                                 int weight_dtype, const void *dY, int lddy, const void *dH, int lddh,
@@ -581,9 +582,11 @@ os2_status os2_linear(int m, int n, int k, int dtype, const void *X, int ldx, co
 /* Its gradient, for dY the gradient of Y (and of R): D = dY act'(pre),
  *   dX = D W,   dW = D^T X,   db = sum over the rows of D,
  * dX (m x k), dW (n x k) of `dtype`, db (n values) of db_dtype (OS2_F32 or `dtype`); each may be NULL.  pre
- * is not read for OS2_ACT_NONE; where it is infinite (rounded, perhaps) act' is its limit, 1 or 0.  D is rounded to `dtype` for the products, not for db (in FP16
- * it is held times 7/8 behind GELU and SiLU: it does not overflow where dY does not); sums
- * are FP32, results rounded once and overwritten; they do not overlap inputs. */
+ * is not read for OS2_ACT_NONE; where it is infinite (rounded, perhaps) act' is its limit, 1 or 0.
+ * D is rounded to `dtype` for the products, which makes dX's and dW's errors 1.4 times those of a D in
+ * FP32, and not for db.  (In FP16 it is held times 7/8 behind GELU and SiLU, whose slopes reach 1.13: it
+ * does not overflow where dY does not.)  Sums are FP32, results rounded once and overwritten; they do
+ * not overlap inputs. */
 size_t os2_linear_backward_workspace_size(int m, int n, int k, const void *X, int ldx,
                                           const void *W, int ldw, const void *dY, int lddy,
                                           int activation);

@@ -6,9 +6,11 @@
 // rho is common to a row and cancels in q, so the integers do not depend on the order of
 // the sum of squares; t, s and t / s are each rounded once in FP32, sums are FP32.
 //
-// Bound by memory: every entry is read once and stays in registers between the sum and the
-// result.  8192 x 8192 BF16: 47 us (5.7 TB/s), with a residual 85 (6.3), int8 74, both 93.  One row
-// is bound by latency: 1.8 us at 4096, 2.1 with a residual.
+// Every entry is read once and stays in registers between the sum and the result.  With a residual
+// memory bounds it: 8192 x 8192 BF16 85 us (6.3 TB/s of what it reads and writes; DRAM 71 % busy, as a
+// copy has it).  Without one (47 us, 5.7 TB/s, DRAM 57 % busy) it is the loads that are in flight and the
+// waits for a row's sum, in 8 bits (74 us, with a residual 93, DRAM 56 %) the instructions of an entry.  One
+// row is bound by latency: 1.8 us at 4096, 2.1 with a residual.
 #include "norm.cuh"
 
 using namespace os2norm;

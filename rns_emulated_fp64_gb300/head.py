@@ -103,7 +103,8 @@ def xent_backward(H: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, lse: t
 class XentFunction(torch.autograd.Function):
     """``xent`` for autograd: XentFunction.apply(H, W, labels, ignore_index) gives
     the losses, row by row; their mean, sum or weights are ordinary operations.
-    The gradient has no gradient of its own: to go back through it raises."""
+    The gradient has no gradient of its own: to go back through it raises, and so do
+    forward mode and vmap."""
 
     @staticmethod
     def forward(ctx, H, W, labels, ignore_index=-100):
@@ -193,7 +194,8 @@ def _in_rows(x):
 
 class RMSNormFunction(torch.autograd.Function):
     """``rmsnorm`` for autograd: RMSNormFunction.apply(X, weight, residual, eps) gives Y, or
-    (Y, H) with a residual.  The gradient has no gradient of its own.  (As with any function
+    (Y, H) with a residual.  The gradient has no gradient of its own, and there is no
+    forward mode and no vmap: they raise.  (As with any function
     of autograd: a backward pass is captured into a graph only while no graph of the same
     leaves lives that was recorded outside of the capture; what autograd keeps of a leaf
     belongs to the stream that it was made on.)"""
@@ -286,7 +288,7 @@ def linear_ways(m: int, n: int, k: int, activation: str = "none", pre: bool = Fa
 
 class LinearFunction(torch.autograd.Function):
     """``linear`` for autograd: LinearFunction.apply(X, W, bias, residual, activation).
-    The gradient has no gradient of its own; captured as ``RMSNormFunction`` is."""
+    No gradient of the gradient, forward mode or vmap, and captured, as ``RMSNormFunction`` is."""
 
     @staticmethod
     def forward(ctx, X, W, bias=None, residual=None, activation="none"):

@@ -153,3 +153,16 @@ def test_the_tested_shapes_go_every_way():
               ("dx", 2, None), ("dw", 1, True), ("dw", 1, False), ("dw", 2, None), ("tokens", 16), ("tokens", 128)}
     wanted |= {(name, c) for name in ("cluster", "dx_cluster") for c in (1, 2, 4, 8)}
     assert wanted <= seen, sorted(wanted - seen, key=str)
+
+
+def test_no_vmap_and_no_forward_mode():
+    """They raise, as the second gradient does, and leave no wrong tangent behind."""
+    import torch.autograd.forward_ad as fwad
+    x, w, g = torch.ones(4, 8, device="cuda").half(), torch.ones(16, 8, device="cuda").half(), torch.ones(8, device="cuda")
+    for f in (lambda x: os2.LinearFunction.apply(x, w), lambda x: os2.RMSNormFunction.apply(x, g),
+              lambda x: os2.XentFunction.apply(x, w, torch.zeros(4, dtype=torch.long, device="cuda"))):
+        with pytest.raises((RuntimeError, NotImplementedError)):
+            torch.func.vmap(f)(x[None].repeat(2, 1, 1))
+        with pytest.raises((RuntimeError, NotImplementedError)):
+            with fwad.dual_level():
+                f(fwad.make_dual(x, torch.ones_like(x)))

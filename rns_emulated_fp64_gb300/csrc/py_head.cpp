@@ -14,7 +14,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/record_function.h>
-#include <c10/core/impl/TorchDispatchModeTLS.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -92,20 +92,29 @@ Tensor vec(PyObject *o, const char *name, int64_t n, at::ScalarType t, c10::Devi
   return x.is_contiguous() ? x : x.contiguous();
 }
 
+// Whether someone looks on in the dispatcher: a dispatch mode (by its key), a profiler, or the filling of new
+// memory that deterministic algorithms ask for.  Asked once a call, and by calls with new outputs only.
+struct Seen {
+  int known = -1;
+  explicit operator bool() {
+    if (known < 0)
+      known = c10::impl::tls_local_dispatch_key_set().included_.has(c10::DispatchKey::Python) || at::hasCallbacks() ||
+              (at::globalContext().deterministicAlgorithms() && at::globalContext().deterministicFillUninitializedMemory());
+    return known;
+  }
+};
+
 // A new output: past the dispatcher, which takes 0.4 us (a norm with a residual of one row 5.4 and
-// 4.5 us a call, 0.1 of it these questions), unless someone looks on there: a dispatch mode, a profiler, or the filling
-// of new memory that deterministic algorithms ask for.
-Tensor fresh(at::IntArrayRef shape, at::ScalarType t, c10::Device dev) {
-  if (c10::impl::TorchDispatchModeTLS::any_modes_set() || at::hasCallbacks() ||
-      (at::globalContext().deterministicAlgorithms() && at::globalContext().deterministicFillUninitializedMemory()))
-    return at::empty(shape, at::TensorOptions().dtype(t).device(dev));
+// 4.4 us a call), unless it is seen there.
+Tensor fresh(Seen &seen, at::IntArrayRef shape, at::ScalarType t, c10::Device dev) {
+  if (seen) return at::empty(shape, at::TensorOptions().dtype(t).device(dev));
   return at::detail::empty_cuda(shape, t, dev, std::nullopt);
 }
 
 // The output, the caller's or a new one, and its leading dimension.
-Tensor out_rows(PyObject *o, const char *name, int64_t m, int64_t n, at::ScalarType t, c10::Device dev, int &ld) {
+Tensor out_rows(Seen &seen, PyObject *o, const char *name, int64_t m, int64_t n, at::ScalarType t, c10::Device dev, int &ld) {
   ld = as_int(std::max<int64_t>(n, 1), name);
-  if (o == Py_None) return fresh({m, n}, t, dev);
+  if (o == Py_None) return fresh(seen, {m, n}, t, dev);
   const Tensor &x = tensor(o, name);
   TORCH_CHECK_VALUE(x.dim() == 2 && x.size(0) == m && x.size(1) == n && x.scalar_type() == t && x.device() == dev, name,
                     " must be (", m, ", ", n, ") ", t, " on ", dev);
@@ -140,8 +149,8 @@ void apart(const Area &out, const char *name, const Area &in, const char *other,
   TORCH_CHECK_VALUE(false, name, " must not overlap ", other);
 }
 
-Tensor out_vec(PyObject *o, const char *name, int64_t n, at::ScalarType t, c10::Device dev) {
-  if (o == Py_None) return fresh({n}, t, dev);
+Tensor out_vec(Seen &seen, PyObject *o, const char *name, int64_t n, at::ScalarType t, c10::Device dev) {
+  if (o == Py_None) return fresh(seen, {n}, t, dev);
   const Tensor &x = tensor(o, name);
   TORCH_CHECK_VALUE(x.dim() == 1 && x.size(0) == n && x.scalar_type() == t && x.device() == dev && x.is_contiguous(), name,
                     " must be ", n, " contiguous ", t, " values on ", dev);
@@ -214,7 +223,8 @@ PyObject *pair(const Tensor &a, const Tensor &b) {  // None for one that is not 
   if (nargs != (count)) {                                                            \
     PyErr_Format(PyExc_TypeError, "%zd arguments, expected %d", nargs, int(count)); \
     return nullptr;                                                                  \
-  }
+  }                                                                                  \
+  [[maybe_unused]] Seen seen;
 
 constexpr const char *kFloats = "float32, float16 or bfloat16", *kHalves = "bfloat16 or float16, one type for H and W";
 
@@ -226,7 +236,7 @@ PyObject *py_quantize_rows(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
   const c10::Device dev = X.device();
   c10::cuda::CUDAGuard on(dev);
   int ldq;
-  const Tensor q = out_rows(a[1], "out", x.m, x.k, at::kChar, dev, ldq), scale = out_vec(a[2], "scale", x.m, at::kFloat, dev);
+  const Tensor q = out_rows(seen, a[1], "out", x.m, x.k, at::kChar, dev, ldq), scale = out_vec(seen, a[2], "scale", x.m, at::kFloat, dev);
   if (!call("os2_quantize_rows", lib.quantize_rows, x.m, x.k, code(X.scalar_type()), (const void *)x.p, x.ld,
             (int8_t *)ptr(q), ldq, (float *)ptr(scale), (void *)c10::cuda::getCurrentCUDAStream(dev.index()).stream()))
     return nullptr;
@@ -260,7 +270,7 @@ PyObject *py_i8(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
   const Tensor sa = linear ? Tensor() : vec(a[1], "a_scale", m, at::kFloat, dev), sb = vec(a[3], "b_scale", n, at::kFloat, dev);
   const Tensor bias = a[4] == Py_None ? Tensor() : vec(a[4], "bias", n, at::kFloat, dev);
   int ldc;
-  const Tensor C = out_rows(a[6], "out", m, n, ct, dev, ldc);
+  const Tensor C = out_rows(seen, a[6], "out", m, n, ct, dev, ldc);
   const Tensor ws = workspace(a[7], lib.i8_workspace(m, n, k, b.p, b.ld), dev, stream);
   const bool ok =
       linear ? call("os2_i8linear", lib.i8linear, m, n, k, code(xt), (const void *)x.p, x.ld, (const int8_t *)b.p, b.ld,
@@ -310,8 +320,8 @@ PyObject *py_xent(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
   const int n = t.h.m, k = t.h.k, v = t.w.m;
   c10::cuda::CUDAGuard on(t.dev);
   const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(t.dev.index());
-  const Tensor y = vec(a[2], "labels", n, at::kLong, t.dev), loss = fresh({n}, at::kFloat, t.dev),
-               lse = fresh({n}, at::kFloat, t.dev);
+  const Tensor y = vec(a[2], "labels", n, at::kLong, t.dev), loss = fresh(seen, {n}, at::kFloat, t.dev),
+               lse = fresh(seen, {n}, at::kFloat, t.dev);
   const Tensor ws = workspace(a[4], lib.xent_workspace(n, k, v, t.w.p, t.w.ld, 0), t.dev, stream);
   if (!call("os2_xent", lib.xent, n, k, v, t.dtype, (const void *)t.h.p, t.h.ld, (const void *)t.w.p, t.w.ld,
             (const long long *)ptr(y), integer(a[3]), (float *)ptr(loss), (float *)ptr(lse), ptr(ws), size_t(ws.nbytes()),
@@ -332,7 +342,7 @@ PyObject *py_xent_backward(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
   const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(t.dev.index());
   const Tensor y = vec(a[2], "labels", n, at::kLong, t.dev), lse = vec(a[3], "lse", n, at::kFloat, t.dev),
                grad = vec(a[4], "grad", n, at::kFloat, t.dev);
-  const Tensor dh = need_dh ? fresh({n, k}, dt, t.dev) : Tensor(), dw = need_dw ? fresh({v, k}, dt, t.dev) : Tensor();
+  const Tensor dh = need_dh ? fresh(seen, {n, k}, dt, t.dev) : Tensor(), dw = need_dw ? fresh(seen, {v, k}, dt, t.dev) : Tensor();
   const Tensor ws = workspace(a[8], lib.xent_workspace(n, k, v, t.w.p, t.w.ld, t.dtype == OS2_BF16 ? OS2_XENT_BACKWARD_BF16 : 1), t.dev, stream);
   if (!call("os2_xent_backward", lib.xent_backward, n, k, v, t.dtype, (const void *)t.h.p, t.h.ld, (const void *)t.w.p,
             t.w.ld, (const long long *)ptr(y), integer(a[5]), (const float *)ptr(lse), (const float *)ptr(grad), ptr(dh), k,
@@ -434,7 +444,7 @@ PyObject *py_adamw_moments(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
   const void *cm = check(a[0], "exp_avg", at::kChar, n), *sm = check(a[1], "exp_avg_scale", at::kFloat, blocks),
              *cv = check(a[2], "exp_avg_sq", at::kByte, n), *sv = check(a[3], "exp_avg_sq_scale", at::kFloat, blocks);
   c10::cuda::CUDAGuard on(dev);
-  const Tensor m = fresh(c.sizes(), at::kFloat, dev), v = fresh(c.sizes(), at::kFloat, dev);
+  const Tensor m = fresh(seen, c.sizes(), at::kFloat, dev), v = fresh(seen, c.sizes(), at::kFloat, dev);
   if (!call("os2_adamw_moments", lib.adamw_moments, (long long)n, (const int8_t *)cm, (const float *)sm, (const uint8_t *)cv,
             (const float *)sv, (float *)ptr(m), (float *)ptr(v),
             (void *)c10::cuda::getCurrentCUDAStream(dev.index()).stream()))
@@ -474,9 +484,9 @@ PyObject *py_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
   const Tensor w = norm_weight(a[1], x.k, t, dev);
   const double eps = real(a[3]);
   int ldy, ldh = std::max(x.k, 1);
-  const Tensor y = out_rows(a[4], "out", x.m, x.k, q8 ? at::kChar : t, dev, ldy);
-  const Tensor h = a[2] == Py_None ? Tensor() : out_rows(a[5], "out_h", x.m, x.k, t, dev, ldh);
-  const Tensor scale = q8 ? out_vec(a[6], "scale", x.m, at::kFloat, dev) : Tensor();
+  const Tensor y = out_rows(seen, a[4], "out", x.m, x.k, q8 ? at::kChar : t, dev, ldy);
+  const Tensor h = a[2] == Py_None ? Tensor() : out_rows(seen, a[5], "out_h", x.m, x.k, t, dev, ldh);
+  const Tensor scale = q8 ? out_vec(seen, a[6], "scale", x.m, at::kFloat, dev) : Tensor();
   const size_t e = X.element_size();
   const bool own_y = a[4] != Py_None, own_h = h.defined() && a[5] != Py_None, own_s = q8 && a[6] != Py_None;
   if (own_y || own_h || own_s) {
@@ -528,7 +538,7 @@ PyObject *py_rmsnorm_backward(PyObject *, PyObject *const *a, Py_ssize_t nargs) 
   c10::cuda::CUDAGuard on(dev);
   const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev.index());
   const Tensor w = norm_weight(a[1], h.k, t, dev);
-  const Tensor dx = need_dx ? fresh({h.m, h.k}, t, dev) : Tensor(), dw = need_dw ? fresh({h.k}, w.scalar_type(), dev) : Tensor();
+  const Tensor dx = need_dx ? fresh(seen, {h.m, h.k}, t, dev) : Tensor(), dw = need_dw ? fresh(seen, {h.k}, w.scalar_type(), dev) : Tensor();
   const Tensor ws = workspace(a[7], need_dw ? lib.rmsnorm_workspace(h.m, h.k) : 0, dev, stream);
   if (!call("os2_rmsnorm_backward", lib.rmsnorm_backward, h.m, h.k, code(t), (const void *)h.p, h.ld, (const void *)ptr(w),
             code(w.scalar_type()), (const void *)dy.p, dy.ld, (const void *)dh.p, dh.ld, eps, ptr(dx), std::max(h.k, 1),
@@ -563,7 +573,7 @@ PyObject *py_sample(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
   const Tensor u = vec(a[1], "u", z.m, at::kFloat, dev), t = setting(a[2], "temperature", z.m, at::kFloat, dev, t0),
                k = setting(a[3], "top_k", z.m, at::kInt, dev, k0), p = setting(a[4], "top_p", z.m, at::kFloat, dev, p0),
                m = setting(a[5], "min_p", z.m, at::kFloat, dev, m0);
-  const Tensor token = fresh({z.m}, at::kLong, dev), logprob = fresh({z.m}, at::kFloat, dev);
+  const Tensor token = fresh(seen, {z.m}, at::kLong, dev), logprob = fresh(seen, {z.m}, at::kFloat, dev);
   if (!call("os2_sample", lib.sample, z.m, z.k, code(Z.scalar_type()), (const void *)z.p, z.ld, (const float *)ptr(u),
             (const float *)ptr(t), t0, (const int *)ptr(k), k0, (const float *)ptr(p), p0, (const float *)ptr(m), m0,
             (long long *)ptr(token), (float *)ptr(logprob), (void *)c10::cuda::getCurrentCUDAStream(dev.index()).stream()))
@@ -590,7 +600,7 @@ PyObject *py_linear(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
                                       : vec(a[2], "bias", n, tensor(a[2], "bias").scalar_type() == t ? t : at::kFloat, dev);
   const Rows r = like(a[3], "residual", Rows{m, n, 0, nullptr}, t, dev);
   int ldy;
-  const Tensor Y = out_rows(a[6], "out", m, n, t, dev, ldy), pre = a[5] == Py_True ? fresh({m, n}, t, dev) : Tensor();
+  const Tensor Y = out_rows(seen, a[6], "out", m, n, t, dev, ldy), pre = a[5] == Py_True ? fresh(seen, {m, n}, t, dev) : Tensor();
   if (a[6] != Py_None) {
     const Area y(Y, ldy);
     apart(y, "out", Area(x, 2), "X");
@@ -631,8 +641,8 @@ PyObject *py_linear_backward(PyObject *, PyObject *const *a, Py_ssize_t nargs) {
   }
   c10::cuda::CUDAGuard on(dev);
   const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev.index());
-  const Tensor dx = need_dx ? fresh({m, k}, t, dev) : Tensor(), dw = need_dw ? fresh({n, k}, t, dev) : Tensor(),
-               db = need_db ? fresh({n}, bt, dev) : Tensor();
+  const Tensor dx = need_dx ? fresh(seen, {m, k}, t, dev) : Tensor(), dw = need_dw ? fresh(seen, {n, k}, t, dev) : Tensor(),
+               db = need_db ? fresh(seen, {n}, bt, dev) : Tensor();
   const Tensor ws = workspace(a[9], lib.linear_backward_workspace(m, n, k, x.p, x.ld, w.p, w.ld, dy.p, dy.ld, act), dev, stream);
   if (!call("os2_linear_backward", lib.linear_backward, m, n, k, code(t), (const void *)x.p, x.ld, (const void *)w.p, w.ld,
             (const void *)dy.p, dy.ld, (const void *)pre.p, pre.ld, act, ptr(dx), std::max(k, 1), ptr(dw), std::max(k, 1), ptr(db),
